@@ -316,9 +316,178 @@ ra_status ra_rope_rotate_quant_noalloc(const ra_problem* p, int in_dtype,
                                        void* stream);
 
 /*
+ * The operators around the attention of a video transformer block: the norm of
+ * queries and keys with their position rotation, a 4-bit key/value cache with
+ * the attention that reads it (frame-by-frame generation), and cross attention
+ * to an encoder's states.
+ *
+ * ra_strides: distances in ELEMENTS between neighbours of a [B, H, N, D] tensor
+ * whose D channels are contiguous; token-major projections [B, N, H, D] are
+ * {N*H*D, D, H*D}.  Every stride of an extent above 1 must be at least 1 and a
+ * multiple of 16 bytes; the stride of an extent of 1 is not looked at.
+ */
+typedef struct {
+  int64_t b, h, n;
+} ra_strides;
+
+typedef enum {
+  RA_NORM_RMS = 0,   /* x / sqrt(mean(x^2) + eps) */
+  RA_NORM_LAYER = 1  /* (x - mean(x)) / sqrt(mean((x - mean(x))^2) + eps) */
+} ra_norm_mode;
+
+/*
+ * The RoPE table of p (grid, seg, theta and rot): one fp32 pair per axis
+ * position and channel pair, (cos, sin), or for RA_ROT_INTERLEAVED the pair
+ * with the rotation in it, ((cos + sin), (cos - sin)) / sqrt(2).  A program
+ * builds it once and keeps it; it depends on nothing but those four fields.
+ *   table   device memory of at least ra_rope_table_bytes(p) bytes (0 if p is
+ *           invalid).
+ */
+size_t ra_rope_table_bytes(const ra_problem* p);
+ra_status ra_rope_table(const ra_problem* p, void* table, size_t bytes, void* stream);
+
+/*
+ * Norm of every head's query and key row, 3D RoPE and the RoPE-aware rotation
+ * (papernotes page, key design 1) in one pass:
+ *   y = norm(x) * weight + bias over the D channels of each row,
+ *   then the RoPE pairs and the rotation p->rot as ra_rope_rotate_quant applies
+ *   them; fp32 throughout, rounded once to bf16.
+ *   Hk           heads of k, >= 1 (p->H is the heads of q).
+ *   norm, eps    ra_norm_mode; eps >= 0.
+ *   in_dtype     element type of q and k.
+ *   q, q_st      [B, H, N, D] and its strides;  k, k_st  [B, Hk, N, D].  q and
+ *                q_out may both be NULL (keys only), or k and k_out.
+ *   *_weight     fp32 [D], NULL for ones;  *_bias  fp32 [D], NULL for zeros.
+ *   pos, table   [N, 3] int32 positions and the table of ra_rope_table for the
+ *                same p.  Both NULL: the norm alone, without RoPE and rotation.
+ *   q_out, k_out bf16 [B, H, N, D] and [B, Hk, N, D], dense.  They must not
+ *                overlap the inputs.
+ */
+ra_status ra_qk_norm_rope(const ra_problem* p, int Hk, int norm, float eps, int in_dtype,
+                          const void* q, const ra_strides* q_st, const void* k, const ra_strides* k_st,
+                          const float* q_weight, const float* k_weight, const float* q_bias,
+                          const float* k_bias, const int32_t* pos, const void* table, void* q_out,
+                          void* k_out, void* stream);
+
+/*
+ * A paged cache of keys and values in 4 bits: per token and head the symmetric
+ * INT4 codes of ra_rope_rotate_quant's Q and K rule (s = fl(amax/7), code =
+ * rint(x * fl(7/amax)) of the exact product, ties to even), for K and V alike.
+ * A row whose amax is below 2^-125 gets s = 0 and codes 0.  Keys go in after
+ * RoPE and, where used, the rotation (queries then carry the same rotation).
+ *   page_size   tokens per page: 16, 32, 64 or 128.
+ *   Hk, D       heads, head dimension (64 or 128).
+ *   k4, v4      [num_pages, Hk, page_size, D/2] packed codes.
+ *   sk, sv      [num_pages, Hk, page_size] fp32 scales.
+ * Token t of sequence b lives in page block_table[b][t / page_size], slot
+ * t % page_size.  block_table is [B, max_pages] int32; entries behind a
+ * sequence's end are not read.  A page outside [0, num_pages) is reported by
+ * ra_sync_status as RA_ERR_INVALID_ARG; nothing outside the cache is touched,
+ * and the results of that sequence are not defined.
+ */
+typedef struct {
+  int num_pages, page_size, Hk, D;
+  uint8_t* k4;
+  float* sk;
+  uint8_t* v4;
+  float* sv;
+} ra_kv4_cache;
+
+/*
+ * Quantises new keys and values into the cache.
+ *   k, v        [B, Hk, T, D] in in_dtype with strides k_st, v_st.
+ *   start       [B] int32: position of each sequence's first new token; NULL: 0.
+ *   n_new       [B] int32: how many of its T rows are new (the rest is padding,
+ *               not read); NULL: all T.
+ * Positions at or past max_pages * page_size, negative starts and counts
+ * outside [0, T] are reported by ra_sync_status; such rows are not written.
+ * Two new rows must not share a slot of a page.
+ */
+ra_status ra_kv4_append(const ra_kv4_cache* c, int in_dtype, int B, int T, const void* k,
+                        const ra_strides* k_st, const void* v, const ra_strides* v_st,
+                        const int32_t* block_table, int max_pages, const int32_t* start,
+                        const int32_t* n_new, void* stream);
+
+/*
+ * Reads tokens back as code * scale: the input of the bf16 paths for layers and
+ * steps that do not attend in 4 bits.
+ *   out_dtype   RA_DT_F32 (exact) or RA_DT_BF16 (rounded once).
+ *   start, n    as for ra_kv4_append: tokens start .. start + n - 1.
+ *   k, v        [B, Hk, T, D] dense; rows at and past n are left as they were.
+ */
+ra_status ra_kv4_read(const ra_kv4_cache* c, int out_dtype, int B, int T, const int32_t* block_table,
+                      int max_pages, const int32_t* start, const int32_t* n, void* k, void* v, void* stream);
+
+/*
+ * Attention over the 4-bit cache: softmax(q k^T * scale) v with k and v the
+ * cached codes times their scales, fp32 softmax and sums, P rounded to bf16
+ * after its scale (codes are exact in bf16).  Forms: one or a few query rows
+ * per key head split the keys over the GPU; many rows run on the tensor cores
+ * in 128-row tiles.
+ *   B, H, Nq    sequences, query heads (a multiple of Hk: query head h reads key
+ *               head h / (H / Hk)), query rows per head.
+ *   max_pages   width of block_table.
+ *   max_len     a bound on seq_lens for planning the split; a longer sequence
+ *               (up to max_pages * page_size) is still computed in full.
+ *   causal      0: every row sees its sequence's seq_len keys.  1: row i of a
+ *               sequence with n rows sees keys 0 .. seq_len - n + i.
+ *   scale       positive; usually 1/sqrt(D).
+ */
+typedef struct {
+  int B, H, Nq, max_pages, max_len, causal;
+  float scale;
+} ra_kv4_attn;
+
+/* Bytes of workspace ra_attn_kv4 needs (0: none, or invalid arguments). */
+size_t ra_attn_kv4_workspace_bytes(const ra_kv4_cache* c, const ra_kv4_attn* a);
+
+/*
+ *   q           [B, H, Nq, D] bf16, dense.
+ *   seq_lens    [B] int32: keys of each sequence, new ones included.
+ *   q_lens      [B] int32: query rows of each sequence; rows behind them are
+ *               neither read nor written.  NULL: all Nq.
+ *   workspace   at least ra_attn_kv4_workspace_bytes; contents on entry do not
+ *               matter; calls that may overlap on the GPU need one each.
+ *   out         [B, H, Nq, D] bf16.  A row without keys gives zeros.
+ *   lse         nullable [B, H, Nq] fp32: log of the row's sum of exponentials,
+ *               -inf for a row without keys.
+ * Lengths outside their range (seq_lens: [0, max_pages * page_size], q_lens:
+ * [0, Nq]) are reported by ra_sync_status and clamped.
+ */
+ra_status ra_attn_kv4(const ra_kv4_cache* c, const ra_kv4_attn* a, const void* q,
+                      const int32_t* block_table, const int32_t* seq_lens, const int32_t* q_lens,
+                      void* workspace, size_t ws_bytes, void* out, float* lse, void* stream);
+
+/*
+ * Cross attention in bf16: softmax(q k^T * scale) v over the states of an
+ * encoder, whose length differs from the queries'.
+ *   B, H, Hk    batch, query heads, key heads (H a multiple of Hk: query head h
+ *               reads key head h / (H / Hk)).
+ *   Nq, Nk, D   query rows, key rows (>= 1), head dimension (64 or 128).
+ *   scale       positive; usually 1/sqrt(D).
+ */
+typedef struct {
+  int B, H, Hk, Nq, Nk, D;
+  float scale;
+} ra_cross_problem;
+
+/*
+ *   q [B, H, Nq, D], k, v [B, Hk, Nk, D], out [B, H, Nq, D]: bf16 with strides.
+ *   kv_lens     [B] int32: keys of each batch entry; key and value rows behind
+ *               them take no part, whatever they hold (NaN too).  NULL: all Nk.
+ *               Lengths outside [0, Nk] are reported by ra_sync_status and
+ *               clamped.  A row without keys gives zeros.
+ *   lse         nullable [B, H, Nq] fp32, dense (-inf for a row without keys).
+ */
+ra_status ra_attn_cross(const ra_cross_problem* p, const void* q, const ra_strides* q_st, const void* k,
+                        const ra_strides* k_st, const void* v, const ra_strides* v_st,
+                        const int32_t* kv_lens, void* out, const ra_strides* out_st, float* lse,
+                        void* stream);
+
+/*
  * Synchronises `stream`, then reads and clears the device status word of the
  * current device.  Returns RA_OK, RA_ERR_INVALID_ARG (a kernel saw a position
- * outside the grid), RA_ERR_TIMEOUT (an internal wait ran past its bound) or
+ * outside the grid, or a page or length out of range), RA_ERR_TIMEOUT (an internal wait ran past its bound) or
  * RA_ERR_CUDA.
  */
 ra_status ra_sync_status(void* stream);

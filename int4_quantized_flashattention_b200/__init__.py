@@ -18,6 +18,8 @@ __all__ = [
     "ROT_NONE", "ROT_INTERLEAVED", "ROT_HALF", "ROT_FULL", "RaError", "Problem", "lib", "workspace_bytes",
     "rope_rotate_quant", "attn_int4", "test_int4_codes", "rope_bf16", "attn_bf16_fallback",
     "attn_int4_qfused", "rope_rotate_quant_s8", "attn_int4_s8", "sync_status", "library_path", "AttnOpts", "P_RANGE", "P_LOCAL_MAX", "P_SYMMETRIC", "L_CODES", "L_FP32",
+    "NORM_RMS", "NORM_LAYER", "rope_table", "qk_norm_rope", "KV4Cache", "kv4_append", "kv4_read", "attn_kv4",
+    "attn_kv4_workspace_bytes", "attn_cross",
 ]
 
 ROT_NONE, ROT_INTERLEAVED, ROT_HALF, ROT_FULL = 0, 1, 2, 3
@@ -90,6 +92,7 @@ def lib():
                      "ra_attn_bf16_fallback", "ra_sync_status", "ra_attn_int4_opts", "ra_test_int4_codes_opts",
                      "ra_attn_int4_qfused", "ra_rope_rotate_quant_s8", "ra_attn_int4_s8"):
             getattr(L, name).restype = C.c_int
+        _block.declare(L)
         _lib = L
     return _lib
 
@@ -347,3 +350,8 @@ def rope_rotate_quant_noalloc(p: Problem, q: torch.Tensor, k: torch.Tensor, v: t
             C.c_void_p(_stream(stream)))
     _check("ra_rope_rotate_quant_noalloc", rc)
     return out
+
+
+from . import _block  # noqa: E402
+from ._block import (NORM_LAYER, NORM_RMS, KV4Cache, attn_cross, attn_kv4,  # noqa: E402
+                     attn_kv4_workspace_bytes, kv4_append, kv4_read, qk_norm_rope, rope_table)

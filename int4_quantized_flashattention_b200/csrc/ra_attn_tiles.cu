@@ -1,0 +1,666 @@
+// Attention in 128-row tiles on the tensor cores: cross attention in bf16 to
+// an encoder's states, and attention of many query rows over the 4-bit cache.
+//   O = softmax(scale q k^T) v, fp32 scores, softmax and sums.
+//
+// One persistent CTA per SM takes two 128-row query tiles of one head (an
+// item) and walks over 128-key blocks; the two tiles share each block and
+// alternate on the tensor cores, one's products running under the other's
+// softmax.
+//   warp 0      TMA producer: Q, and (cross) K and V, 64-channel boxes with the
+//               128-byte swizzle
+//   warps 1, 2  MMA issuers of tiles 0 and 1: S = Q K^T into TMEM (tcgen05
+//               kind::f16, M = N = 128), then O += P V with P read from TMEM
+//   warp 3      (cross) clears value rows behind the last key, which may hold
+//               anything, before the MMA reads them: 0 * NaN is not 0
+//   warps 4-7   (cache) unpack codes into bf16 K and V tiles (exact); a thread
+//               per key, the next block's codes in flight in its registers
+//   then 4 + 4  softmax warps, one row per thread: no exchange between threads.
+// P overwrites the S columns it came from, so the next S of the tile follows
+// P V.  The reference maximum moves only when a score passes it by 2^8
+// (kLazy): rescaling O in TMEM is rare, and P stays below 2^8, which bf16
+// holds as well as 1.  The scales of the cache multiply the scores (keys) and
+// P before its rounding (values) in fp32.
+#include <cuda.h>
+#include <cudaTypedefs.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "ra_common.cuh"
+#include "ra_tmem_row.cuh"
+#include "ra_block.h"
+#include "ra_kv4.cuh"
+
+namespace ra {
+namespace {
+
+__device__ uint32_t g_tiles_status = 0;
+
+constexpr int kRows = 128;   // query rows per tile = MMA M
+constexpr int kTiles = 2;    // query tiles per CTA
+constexpr int kKeys = 128;   // keys per block = MMA N of S
+constexpr float kLazy = 8.0f;
+
+template <int D, bool KV4>
+struct CfgT {
+  static constexpr int kHalves = D / 64;
+  static constexpr int kHalf = kRows * 128;            // one 64-channel box of 128 rows
+  static constexpr int kTileBytes = kRows * D * 2;     // a Q, K or V tile
+  static constexpr int kStages = 2;                    // of K, and of V
+  static constexpr int oQ = 0;
+  static constexpr int oK = oQ + kTiles * kTileBytes;
+  static constexpr int oV = oK + kStages * kTileBytes;
+  static constexpr int oScale = oV + kStages * kTileBytes;      // [sk | sv][stage][key], cache only
+  static constexpr int oBar = oScale + (KV4 ? 2 * kStages * kKeys * 4 : 0);
+  static constexpr int kNumBars = 2 + 2 + 5 * kStages + 2 + 2 + 2 + 2;
+  static constexpr int oMisc = oBar + kNumBars * 8;
+  static constexpr int kSmem = oMisc + 16 + 1024;
+  static constexpr int kFirstSoftmax = KV4 ? 8 : 4;
+  static constexpr int kThreads = (kFirstSoftmax + 8) * 32;
+  static constexpr uint32_t kIdescQK = instr_desc(kCfmtF32, 1, 1, 0, 0, kRows, kKeys);
+  static constexpr uint32_t kIdescPV = instr_desc(kCfmtF32, 1, 1, 0, 1, kRows, D);
+  static_assert(kSmem <= 232448, "shared memory");
+};
+
+struct TileArgs {
+  int heads;        // heads that items run over: query heads (cross) or key heads (cache)
+  int group;        // cross: query heads per key head; cache: unused
+  int R;            // query rows per head of an item
+  int npairs, nsplit, nitems;
+  float scale_log2;
+  __nv_bfloat16* out;
+  ra_strides os;
+  float* lse;
+  const int32_t* kv_lens;   // cross: may be NULL; cache: seq_lens
+  // cross
+  int Nk;
+  // cache
+  const int32_t* q_lens;
+  const int32_t* table;
+  const uint8_t* k4;
+  const float* sk;
+  const uint8_t* v4;
+  const float* sv;
+  int num_pages, page_log2, max_pages, Nq, causal;
+  Kv4Parts parts;
+};
+
+struct Item {
+  int b, h, row0, split;
+  int len, ql;      // keys and query rows of the sequence
+  int k0, nb;       // first key and number of the item's key blocks
+};
+
+template <bool KV4>
+__device__ __forceinline__ Item get_item(const TileArgs& a, int item, uint32_t* bad) {
+  Item it;
+  const int pair = item % a.npairs, rest = item / a.npairs;
+  it.split = rest % a.nsplit;
+  const int bh = rest / a.nsplit;
+  it.b = bh / a.heads;
+  it.h = bh % a.heads;
+  it.row0 = pair * kTiles * kRows;
+  it.ql = a.R;
+  int end;
+  if constexpr (KV4) {
+    it.len = clamp_len(__ldg(a.kv_lens + it.b), a.max_pages << a.page_log2, bad);
+    it.ql = a.q_lens ? clamp_len(__ldg(a.q_lens + it.b), a.Nq, bad) : a.Nq;
+    end = it.len;
+    if (a.causal) {  // the furthest key that a row of the item sees
+      const int last = min(it.row0 + kTiles * kRows, a.R) - 1;
+      if (it.row0 / a.Nq == last / a.Nq) end = max(0, min(end, it.len - it.ql + last % a.Nq + 1));
+    }
+  } else {
+    it.len = a.kv_lens ? clamp_len(__ldg(a.kv_lens + it.b), a.Nk, bad) : a.Nk;
+    end = it.len;
+  }
+  const int blocks = (end + kKeys - 1) / kKeys;
+  const int per = (blocks + a.nsplit - 1) / a.nsplit;
+  const int first = min(it.split * per, blocks);
+  it.k0 = first * kKeys;
+  it.nb = min(per, blocks - first);
+  return it;
+}
+
+__device__ __forceinline__ bool wait_t(uint64_t* bar, uint32_t parity, volatile int* abort, uint32_t backoff_ns = 16) {
+  return mbar_wait_ex(bar, parity, abort, backoff_ns) > 0;
+}
+
+// The same for a whole warp: every lane waits, and all of them go on or none (a
+// wait that gave up must not part the warp before its collectives).
+__device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, volatile int* abort, uint32_t backoff_ns = 16) {
+  const bool got = wait_t(bar, parity, abort, backoff_ns);
+  return __all_sync(0xFFFFFFFFu, got);
+}
+
+__device__ __forceinline__ float max3t(float a, float b, float c) { return fmaxf(a, fmaxf(b, c)); }
+
+template <int D, bool KV4>
+__global__ void __launch_bounds__(CfgT<D, KV4>::kThreads, 1)
+attn_tiles_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                  const __grid_constant__ CUtensorMap tm_v, const TileArgs a) {
+  using C = CfgT<D, KV4>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  uint64_t* b = reinterpret_cast<uint64_t*>(smem + C::oBar);
+  uint64_t* const q_full = b; b += 2;              // [tile]
+  uint64_t* const q_free = b; b += 2;
+  uint64_t* const k_full = b; b += C::kStages;
+  uint64_t* const k_empty = b; b += C::kStages;
+  uint64_t* const v_full = b; b += C::kStages;     // cross: the copy has landed
+  uint64_t* const v_ready = b; b += C::kStages;    // the MMA may read
+  uint64_t* const v_empty = b; b += C::kStages;
+  uint64_t* const s_full = b; b += 2;              // [tile]
+  uint64_t* const p_full = b; b += 2;
+  uint64_t* const pv_done = b; b += 2;
+  uint64_t* const drain = b;
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + C::oMisc);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::oMisc + 4);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(q_full + i, 1); mbar_init(q_free + i, 1);
+      mbar_init(s_full + i, 1); mbar_init(p_full + i, 4); mbar_init(pv_done + i, 1); mbar_init(drain + i, 1);
+    }
+    for (int i = 0; i < C::kStages; ++i) {
+      // cache: four unpacking warps fill a stage; the softmax warps read its scales
+      mbar_init(k_full + i, KV4 ? 4 : 1); mbar_init(k_empty + i, KV4 ? 2 + 8 : 2);
+      mbar_init(v_full + i, 1); mbar_init(v_ready + i, KV4 ? 4 : 1); mbar_init(v_empty + i, KV4 ? 2 + 8 : 2);
+    }
+    *abort_flag = 0;
+    fence_barrier_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(tmem_holder, 512);
+    tmem_relinquish();
+  }
+  if (warp == 0 && lane == 0) {
+    prefetch_tmap(&tm_q);
+    if (!KV4) { prefetch_tmap(&tm_k); prefetch_tmap(&tm_v); }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tbase = *tmem_holder;
+  float* const scales = reinterpret_cast<float*>(smem + C::oScale);
+  uint32_t bad = 0;
+  bool ok = true;
+  if (warp < 4) {
+    if constexpr (KV4) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+    else asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    if (warp == 0 && lane == 0) {
+      // ------------------------------------------------------------ TMA producer
+      uint32_t g = 0, li = 0;
+      for (int item = blockIdx.x; item < a.nitems && ok; item += gridDim.x) {
+        const Item it = get_item<KV4>(a, item, &bad);
+        if (it.nb == 0) continue;
+        auto load_q = [&]() {
+          for (int tt = 0; tt < kTiles && ok; ++tt) {
+            if (!(ok = wait_t(q_free + tt, (li & 1) ^ 1, abort_flag, 64u))) return;
+            mbar_arrive_expect_tx(q_full + tt, C::kTileBytes);
+            for (int h = 0; h < C::kHalves; ++h)
+              tma_load_4d(smem + C::oQ + tt * C::kTileBytes + h * C::kHalf, &tm_q, q_full + tt, h * 64,
+                          it.row0 + tt * kRows, it.h, it.b);
+          }
+          ++li;
+        };
+        if constexpr (KV4) {
+          load_q();
+        } else {
+          const int hk = it.h / a.group;
+          for (int t = 0; t < it.nb && ok; ++t, ++g) {
+            const int s = g % C::kStages, key = it.k0 + t * kKeys;
+            const uint32_t par = ((g / C::kStages) & 1) ^ 1;
+            if (!(ok = wait_t(k_empty + s, par, abort_flag, 64u))) break;
+            mbar_arrive_expect_tx(k_full + s, C::kTileBytes);
+            for (int h = 0; h < C::kHalves; ++h)
+              tma_load_4d(smem + C::oK + s * C::kTileBytes + h * C::kHalf, &tm_k, k_full + s, h * 64, key, hk, it.b);
+            if (t == 0) {
+              load_q();
+              if (!ok) break;
+            }
+            if (!(ok = wait_t(v_empty + s, par, abort_flag, 64u))) break;
+            mbar_arrive_expect_tx(v_full + s, C::kTileBytes);
+            for (int h = 0; h < C::kHalves; ++h)
+              tma_load_4d(smem + C::oV + s * C::kTileBytes + h * C::kHalf, &tm_v, v_full + s, h * 64, key, hk, it.b);
+          }
+        }
+      }
+      // Wait (bounded) for the copies of the last stages and of Q to land.
+      uint32_t n = 0;
+      if (!KV4)
+        for (uint32_t k = (g > (uint32_t)C::kStages ? g - C::kStages : 0); k < g; ++k) {
+          while (!mbar_try_wait(k_full + (k % C::kStages), (k / C::kStages) & 1) && ++n < kSpinLimit) {}
+          while (!mbar_try_wait(v_full + (k % C::kStages), (k / C::kStages) & 1) && ++n < kSpinLimit) {}
+        }
+      if (li > 0)
+        for (int tt = 0; tt < kTiles; ++tt)
+          while (!mbar_try_wait(q_full + tt, (li - 1) & 1) && ++n < kSpinLimit) {}
+    } else if ((warp == 1 || warp == 2) && lane == 0) {
+      // ------------------------------------------------------------ MMA issuers
+      const int tt = warp - 1;
+      const uint32_t sQ = smem_u32(smem + C::oQ) + tt * C::kTileBytes;
+      const uint32_t sK = smem_u32(smem + C::oK), sV = smem_u32(smem + C::oV);
+      const uint32_t tS = tbase + tt * 128, tO = tbase + 256 + tt * 128;
+      uint32_t g = 0, li = 0;
+      for (int item = blockIdx.x; item < a.nitems && ok; item += gridDim.x) {
+        const Item it = get_item<KV4>(a, item, &bad);
+        if (it.nb == 0) continue;
+        if (!(ok = wait_t(q_full + tt, li & 1, abort_flag, 32u))) break;
+        ++li;
+        for (int t = 0; t < it.nb; ++t, ++g) {
+          const int s = g % C::kStages;
+          const uint32_t par = (g / C::kStages) & 1;
+          if (!(ok = wait_t(k_full + s, par, abort_flag, 32u))) break;
+          // S takes the columns of the previous block's P.
+          if (g > 0 && !(ok = wait_t(pv_done + tt, (g - 1) & 1, abort_flag, 32u))) break;
+          tc_fence_after();
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const uint32_t off = (kk >> 2) * C::kHalf + (kk & 3) * 32;
+            mma_f16_ss(tS, smem_desc(sQ + off, 16, 1024, kSwizzle128B),
+                       smem_desc(sK + s * C::kTileBytes + off, 16, 1024, kSwizzle128B), C::kIdescQK, kk > 0 ? 1u : 0u);
+          }
+          mma_commit(s_full + tt);
+          mma_commit(k_empty + s);
+          if (t == it.nb - 1) mma_commit(q_free + tt);
+          if (!(ok = wait_t(v_ready + s, par, abort_flag, 32u))) break;
+          if (!(ok = wait_t(p_full + tt, g & 1, abort_flag, 32u))) break;
+          tc_fence_after();
+#pragma unroll
+          for (int kk = 0; kk < kKeys / 16; ++kk)
+            mma_f16_ts(tO, tS + kk * 8, smem_desc(sV + s * C::kTileBytes + kk * 16 * 128, C::kHalf, 1024, kSwizzle128B),
+                       C::kIdescPV, t > 0 || kk > 0 ? 1u : 0u);
+          mma_commit(pv_done + tt);
+          mma_commit(v_empty + s);
+        }
+      }
+      mma_commit(drain + tt);
+      uint32_t n = 0;
+      while (!mbar_try_wait(drain + tt, 0) && ++n < kSpinLimit) {}
+    } else if (warp == 3 && !KV4) {
+      // ------------------------------------------------------------ value rows behind the last key
+      uint32_t g = 0;
+      for (int item = blockIdx.x; item < a.nitems && ok; item += gridDim.x) {
+        const Item it = get_item<KV4>(a, item, &bad);
+        for (int t = 0; t < it.nb; ++t, ++g) {
+          const int s = g % C::kStages;
+          if (!(ok = wait_warp(v_full + s, (g / C::kStages) & 1, abort_flag, 64u))) break;
+          // Rows past Nk are zeros already (filled by the copy).
+          const int first = it.len - (it.k0 + t * kKeys), last = min(kKeys, a.Nk - (it.k0 + t * kKeys));
+          if (first < last) {
+            for (int idx = lane; idx < (last - first) * C::kHalves * 8; idx += 32) {
+              const int row = first + idx / (C::kHalves * 8), ch = idx % (C::kHalves * 8);
+              *reinterpret_cast<uint4*>(smem + C::oV + s * C::kTileBytes + (ch >> 3) * C::kHalf + row * 128 +
+                                        (ch & 7) * 16) = make_uint4(0, 0, 0, 0);
+            }
+            fence_proxy_async_smem();
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(v_ready + s);
+        }
+      }
+    }
+  } else if (KV4 && warp < 8) {
+    // -------------------------------------------------------------- unpacking warps
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
+    if constexpr (KV4) {
+      constexpr int kQ = D / 32;  // 16-byte pieces of a code row
+      const int row = threadIdx.x - 128;
+      uint4 kr[kQ], vr[kQ];
+      float ks = 0.0f, vs = 0.0f;
+      auto fetch = [&](const Item& it, int t) {
+        const int key = it.k0 + t * kKeys + row;
+#pragma unroll
+        for (int i = 0; i < kQ; ++i) kr[i] = vr[i] = make_uint4(0, 0, 0, 0);
+        ks = vs = 0.0f;
+        if (key < it.len) {
+          int page = __ldg(a.table + static_cast<size_t>(it.b) * a.max_pages + (key >> a.page_log2));
+          if (page < 0 || page >= a.num_pages) {
+            bad |= kStatusBadPosition;
+            page = 0;
+          }
+          const size_t at = ((static_cast<size_t>(page) * a.heads + it.h) << a.page_log2) + (key & ((1 << a.page_log2) - 1));
+          const uint4* kp = reinterpret_cast<const uint4*>(a.k4 + at * (D / 2));
+          const uint4* vp = reinterpret_cast<const uint4*>(a.v4 + at * (D / 2));
+#pragma unroll
+          for (int i = 0; i < kQ; ++i) {
+            kr[i] = __ldg(kp + i);
+            vr[i] = __ldg(vp + i);
+          }
+          ks = __ldg(a.sk + at);
+          vs = __ldg(a.sv + at);
+        }
+      };
+      uint32_t g = 0;
+      for (int item = blockIdx.x; item < a.nitems && ok; item += gridDim.x) {
+        const Item it = get_item<KV4>(a, item, &bad);
+        if (it.nb > 0) fetch(it, 0);
+        for (int t = 0; t < it.nb; ++t, ++g) {
+          uint4 k[kQ], v[kQ];
+#pragma unroll
+          for (int i = 0; i < kQ; ++i) {
+            k[i] = kr[i];
+            v[i] = vr[i];
+          }
+          const float ks_now = ks, vs_now = vs;
+          if (t + 1 < it.nb) fetch(it, t + 1);
+          const int s = g % C::kStages;
+          const uint32_t par = ((g / C::kStages) & 1) ^ 1;
+          if (!(ok = wait_warp(k_empty + s, par, abort_flag, 64u))) break;
+          uint8_t* const kt = smem + C::oK + s * C::kTileBytes + row * 128;
+          uint8_t* const vt = smem + C::oV + s * C::kTileBytes + row * 128;
+#pragma unroll
+          for (int i = 0; i < kQ; ++i) {
+            const uint32_t w[4] = {k[i].x, k[i].y, k[i].z, k[i].w};
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {  // eight channels in their order
+              const uint32_t p0 = codes_bf16(w[c]), p1 = codes_bf16(w[c] >> 4);
+              const uint32_t p2 = codes_bf16(w[c] >> 8), p3 = codes_bf16(w[c] >> 12);
+              const uint4 o = make_uint4(__byte_perm(p0, p1, 0x5410), __byte_perm(p2, p3, 0x5410),
+                                         __byte_perm(p0, p1, 0x7632), __byte_perm(p2, p3, 0x7632));
+              const int ch = i * 4 + c;
+              *reinterpret_cast<uint4*>(kt + (ch >> 3) * C::kHalf + (((ch & 7) ^ (row & 7)) << 4)) = o;
+            }
+          }
+          scales[s * kKeys + row] = ks_now * a.scale_log2;
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(k_full + s);
+          if (!(ok = wait_warp(v_empty + s, par, abort_flag, 64u))) break;
+#pragma unroll
+          for (int i = 0; i < kQ; ++i) {
+            const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {  // channels 0 4 1 5 2 6 3 7 of eight; the epilogue puts them right
+              const uint4 o = make_uint4(codes_bf16(w[c]), codes_bf16(w[c] >> 4), codes_bf16(w[c] >> 8),
+                                         codes_bf16(w[c] >> 12));
+              const int ch = i * 4 + c;
+              *reinterpret_cast<uint4*>(vt + (ch >> 3) * C::kHalf + (((ch & 7) ^ (row & 7)) << 4)) = o;
+            }
+          }
+          scales[(C::kStages + s) * kKeys + row] = vs_now;
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(v_ready + s);
+        }
+      }
+    }
+  } else {
+    // -------------------------------------------------------------- softmax, one row per thread
+    if constexpr (KV4) asm volatile("setmaxnreg.inc.sync.aligned.u32 176;");
+    else asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
+    const int tt = (warp - C::kFirstSoftmax) >> 2;
+    const int quad = warp & 3;
+    const uint32_t lane_off = static_cast<uint32_t>(quad * 32) << 16;
+    const uint32_t tS = tbase + tt * 128 + lane_off, tO = tbase + 256 + tt * 128 + lane_off;
+    uint32_t g = 0;
+    for (int item = blockIdx.x; item < a.nitems && ok; item += gridDim.x) {
+      const Item it = get_item<KV4>(a, item, &bad);
+      const int r = it.row0 + tt * kRows + quad * 32 + lane;
+      int lim = it.len;
+      bool row_live = r < a.R;
+      if constexpr (KV4) {
+        const int i = r % a.Nq;
+        row_live = row_live && i < it.ql;
+        if (a.causal) lim = max(0, it.len - it.ql + i + 1);
+      }
+      float m = -INFINITY, l = 0.0f;
+      for (int t = 0; t < it.nb; ++t, ++g) {
+        if (!(ok = wait_warp(s_full + tt, g & 1, abort_flag))) break;
+        tc_fence_after();
+        uint32_t raw[kKeys];
+        tmem_ld_row<kKeys>(tS, raw);
+        float* const s = reinterpret_cast<float*>(raw);
+        const int stg = g % C::kStages;
+        if constexpr (KV4) {
+          const float4* const sc = reinterpret_cast<const float4*>(scales + stg * kKeys);
+#pragma unroll
+          for (int j = 0; j < kKeys / 4; ++j) {
+            const float4 f = sc[j];
+            const float2 lo = __fmul2_rn(make_float2(s[4 * j], s[4 * j + 1]), make_float2(f.x, f.y));
+            const float2 hi = __fmul2_rn(make_float2(s[4 * j + 2], s[4 * j + 3]), make_float2(f.z, f.w));
+            s[4 * j] = lo.x; s[4 * j + 1] = lo.y; s[4 * j + 2] = hi.x; s[4 * j + 3] = hi.y;
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(k_empty + stg);
+        }
+        const int left = lim - (it.k0 + t * kKeys);  // keys of this block that the row sees
+        if (left < kKeys) {
+#pragma unroll
+          for (int j = 0; j < kKeys; ++j)
+            if (j >= left) s[j] = -INFINITY;
+        }
+        float top[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          top[q] = s[q];
+#pragma unroll
+          for (int j = 4; j + 4 < kKeys; j += 8) top[q] = max3t(top[q], s[j + q], s[j + 4 + q]);
+          top[q] = fmaxf(top[q], s[kKeys - 4 + q]);
+        }
+        float mb = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+        if constexpr (!KV4) mb *= a.scale_log2;
+        // The reference moves on the first block and when passed by kLazy.
+        const bool up = mb > m + kLazy;
+        const float f = up ? ex2_approx(m - mb) : 1.0f;
+        const bool any_up = __any_sync(0xFFFFFFFFu, up);
+        if (up) {
+          m = mb;
+          l *= f;
+        }
+        if (any_up && t > 0) {
+          const float2 f2 = make_float2(f, f);
+#pragma unroll
+          for (int c = 0; c < D; c += 32) {
+            uint32_t o[32];
+            tmem_ld_row<32>(tO + c, o);
+#pragma unroll
+            for (int i = 0; i < 32; i += 2) {
+              const float2 x = __fmul2_rn(make_float2(__uint_as_float(o[i]), __uint_as_float(o[i + 1])), f2);
+              o[i] = __float_as_uint(x.x);
+              o[i + 1] = __float_as_uint(x.y);
+            }
+            tmem_st_row_nw<32>(tO + c, o);
+          }
+        }
+        const float mr = m == -INFINITY ? 0.0f : m;
+        const float2 c2 = make_float2(a.scale_log2, a.scale_log2), m2 = make_float2(-mr, -mr);
+        float2 sum2 = make_float2(0.0f, 0.0f);
+#pragma unroll
+        for (int c = 0; c < kKeys; c += 32) {
+          uint32_t w[16];
+          if (KV4 && c == 0) {
+            if (!(ok = wait_warp(v_ready + stg, (g / C::kStages) & 1, abort_flag))) break;
+          }
+#pragma unroll
+          for (int j = 0; j < 32; j += 4) {
+            float2 x = make_float2(s[c + j], s[c + j + 1]), y = make_float2(s[c + j + 2], s[c + j + 3]);
+            if constexpr (KV4) {
+              x = __fadd2_rn(x, m2);
+              y = __fadd2_rn(y, m2);
+            } else {
+              x = __ffma2_rn(x, c2, m2);
+              y = __ffma2_rn(y, c2, m2);
+            }
+            x = make_float2(ex2_approx(x.x), ex2_approx(x.y));
+            y = make_float2(ex2_approx(y.x), ex2_approx(y.y));
+            sum2 = __fadd2_rn(sum2, x);
+            sum2 = __fadd2_rn(sum2, y);
+            if constexpr (KV4) {
+              const float4 f4 = *reinterpret_cast<const float4*>(scales + (C::kStages + stg) * kKeys + c + j);
+              x = __fmul2_rn(x, make_float2(f4.x, f4.y));
+              y = __fmul2_rn(y, make_float2(f4.z, f4.w));
+            }
+            w[j / 2] = pack_bf16(x.x, x.y);
+            w[j / 2 + 1] = pack_bf16(y.x, y.y);
+          }
+          tmem_st_row_nw<16>(tS + c / 2, w);
+        }
+        if (!ok) break;
+        l += sum2.x + sum2.y;
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(p_full + tt);
+          if constexpr (KV4) mbar_arrive(v_empty + stg);
+        }
+      }
+      if (!ok) break;
+      if (it.nb > 0) {
+        if (!(ok = wait_warp(pv_done + tt, (g - 1) & 1, abort_flag))) break;
+        tc_fence_after();
+      }
+      const bool some = m != -INFINITY;
+      const float inv = some ? 1.0f / l : 0.0f;
+      const float lse2 = some ? m + log2f(l) : -INFINITY;
+      const size_t bh = static_cast<size_t>(it.b) * a.heads + it.h;
+      const size_t at = bh * a.R + r;
+      const bool split = KV4 && a.nsplit > 1;
+      const size_t prow = static_cast<size_t>(it.split) * (a.nitems / (a.npairs * a.nsplit)) * a.R + at;
+      __nv_bfloat16* const orow = a.out + it.b * a.os.b + it.h * a.os.h + r * a.os.n;
+#pragma unroll
+      for (int c = 0; c < D; c += 32) {
+        uint32_t o[32];
+        if (it.nb > 0) {
+          tmem_ld_row<32>(tO + c, o);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) o[i] = 0u;
+        }
+        float x[32];
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+          // cache: column 2i + e of eight holds channel i + 4e
+          const int from = KV4 ? (i & ~7) + 2 * (i & 3) + ((i >> 2) & 1) : i;
+          x[i] = __uint_as_float(o[from]) * inv;
+          if (!some) x[i] = 0.0f;
+        }
+        if (row_live && split) {
+          float4* const dst = reinterpret_cast<float4*>(a.parts.o + prow * D + c);
+#pragma unroll
+          for (int i = 0; i < 32; i += 4) dst[i / 4] = make_float4(x[i], x[i + 1], x[i + 2], x[i + 3]);
+        } else if (row_live) {
+#pragma unroll
+          for (int i = 0; i < 32; i += 8)
+            *reinterpret_cast<uint4*>(orow + c + i) =
+                make_uint4(pack_bf16(x[i], x[i + 1]), pack_bf16(x[i + 2], x[i + 3]), pack_bf16(x[i + 4], x[i + 5]),
+                           pack_bf16(x[i + 6], x[i + 7]));
+        }
+        __syncwarp();
+      }
+      tc_fence_before();
+      if (row_live) {
+        if (split) a.parts.lse2[prow] = lse2;
+        else if (a.lse) a.lse[at] = lse2 * kLn2;
+      }
+    }
+  }
+  if (!ok) bad |= kStatusTimeout;
+  if (bad) atomicOr(&g_tiles_status, bad);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 1) tmem_dealloc(tbase, 512);
+}
+
+// ------------------------------------------------------------------ host side
+PFN_cuTensorMapEncodeTiled_v12000 get_encoder_t() {
+  static PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
+    cudaDriverEntryPointQueryResult q;
+    void* p = nullptr;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess)
+      p = nullptr;
+    return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+  }();
+  return fn;
+}
+
+// 4D map over bf16 [B, H, N, D] with strides; box = 64 channels x 128 rows,
+// 128-byte swizzle, zeros past N.
+bool make_map(CUtensorMap* m, const void* base, int B, int H, int N, int D, const ra_strides& st) {
+  auto enc = get_encoder_t();
+  if (!enc) return false;
+  // The stride of an extent of one is free; the map wants a valid one.
+  const int64_t row = static_cast<int64_t>(D);
+  const int64_t sn = N > 1 ? st.n : row, sh = H > 1 ? st.h : row, sb = B > 1 ? st.b : row;
+  cuuint64_t dims[4] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(N), static_cast<cuuint64_t>(H),
+                        static_cast<cuuint64_t>(B)};
+  cuuint64_t strides[3] = {static_cast<cuuint64_t>(sn) * 2, static_cast<cuuint64_t>(sh) * 2,
+                           static_cast<cuuint64_t>(sb) * 2};
+  cuuint32_t box[4] = {64, static_cast<cuuint32_t>(kRows), 1, 1};
+  cuuint32_t es[4] = {1, 1, 1, 1};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides, box, es,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int D, bool KV4>
+cudaError_t launch_tiles(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv, const TileArgs& a,
+                         cudaStream_t st) {
+  using C = CfgT<D, KV4>;
+  auto kern = attn_tiles_kernel<D, KV4>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+  if (e != cudaSuccess) return e;
+  kern<<<a.nitems < kNumSMs ? a.nitems : kNumSMs, C::kThreads, C::kSmem, st>>>(mq, mk, mv, a);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_kv4_tiles(const ra_kv4_cache& c, const ra_kv4_attn& at, const Kv4Plan& plan, const void* q,
+                             const int32_t* table, const int32_t* seq_lens, const int32_t* q_lens,
+                             const Kv4Parts& parts, void* out, float* lse, cudaStream_t st) {
+  TileArgs a{};
+  a.heads = c.Hk; a.group = 1; a.R = at.H / c.Hk * at.Nq;
+  a.npairs = (a.R + kTiles * kRows - 1) / (kTiles * kRows);
+  a.nsplit = plan.nsplit;
+  a.nitems = at.B * c.Hk * a.nsplit * a.npairs;
+  a.scale_log2 = at.scale * kLog2e;
+  a.out = static_cast<__nv_bfloat16*>(out);
+  a.os.n = c.D;
+  a.os.h = static_cast<int64_t>(a.R) * c.D;
+  a.os.b = a.os.h * c.Hk;
+  a.lse = lse;
+  a.kv_lens = seq_lens; a.q_lens = q_lens; a.table = table;
+  a.k4 = c.k4; a.sk = c.sk; a.v4 = c.v4; a.sv = c.sv;
+  a.num_pages = c.num_pages; a.page_log2 = __builtin_ctz(static_cast<unsigned>(c.page_size));
+  a.max_pages = at.max_pages; a.Nq = at.Nq; a.causal = at.causal;
+  a.parts = parts;
+  CUtensorMap mq;
+  if (!make_map(&mq, q, at.B, c.Hk, a.R, c.D, a.os)) return cudaErrorInvalidValue;
+  return c.D == 64 ? launch_tiles<64, true>(mq, mq, mq, a, st) : launch_tiles<128, true>(mq, mq, mq, a, st);
+}
+
+cudaError_t launch_attn_cross(const ra_cross_problem& p, const void* q, const ra_strides& qs, const void* k,
+                              const ra_strides& ks, const void* v, const ra_strides& vs, const int32_t* kv_lens,
+                              void* out, const ra_strides& os, float* lse, cudaStream_t st) {
+  TileArgs a{};
+  a.heads = p.H; a.group = p.H / p.Hk; a.R = p.Nq;
+  a.npairs = (a.R + kTiles * kRows - 1) / (kTiles * kRows);
+  a.nsplit = 1;
+  a.nitems = p.B * p.H * a.npairs;
+  a.scale_log2 = p.scale * kLog2e;
+  a.out = static_cast<__nv_bfloat16*>(out);
+  a.os = os;
+  a.lse = lse;
+  a.kv_lens = kv_lens;
+  a.Nk = p.Nk;
+  CUtensorMap mq, mk, mv;
+  if (!make_map(&mq, q, p.B, p.H, p.Nq, p.D, qs) || !make_map(&mk, k, p.B, p.Hk, p.Nk, p.D, ks) ||
+      !make_map(&mv, v, p.B, p.Hk, p.Nk, p.D, vs))
+    return cudaErrorInvalidValue;
+  return p.D == 64 ? launch_tiles<64, false>(mq, mk, mv, a, st) : launch_tiles<128, false>(mq, mk, mv, a, st);
+}
+
+cudaError_t read_tiles_status(uint32_t* out) {
+  uint32_t zero = 0;
+  cudaError_t e = cudaMemcpyFromSymbol(out, g_tiles_status, sizeof(uint32_t));
+  if (e != cudaSuccess) return e;
+  return cudaMemcpyToSymbol(g_tiles_status, &zero, sizeof(uint32_t));
+}
+
+}  // namespace ra

@@ -1,0 +1,70 @@
+// Internal interface of the operators around the attention: norm + RoPE, the
+// 4-bit key/value cache, attention over it and cross attention.
+#pragma once
+
+#include <cuda_runtime.h>
+
+#include <cstddef>
+#include <cstdint>
+
+#include "../../include/ra.h"
+
+namespace ra {
+
+constexpr int kNumSMs = 148;  // B200: the split of a call is planned for this many SMs
+
+// ---------------------------------------------------------------- norm + RoPE
+struct NormRopeCall {
+  const void* x[2];  // q, k (NULL: absent)
+  ra_strides st[2];
+  const float* weight[2];
+  const float* bias[2];
+  void* out[2];
+  int heads[2];
+  int norm, dtype;
+  float eps;
+  const int32_t* pos;
+  const float2* tab;
+};
+cudaError_t launch_norm_rope(const ra_problem& p, const NormRopeCall& c, cudaStream_t st);
+cudaError_t read_norm_rope_status(uint32_t* out);
+
+// ---------------------------------------------------------------- 4-bit cache
+cudaError_t launch_kv4_append(const ra_kv4_cache& c, int dtype, int B, int T, const void* k, const ra_strides& ks,
+                              const void* v, const ra_strides& vs, const int32_t* table, int max_pages,
+                              const int32_t* start, const int32_t* n_new, cudaStream_t st);
+cudaError_t launch_kv4_read(const ra_kv4_cache& c, int dtype, int B, int T, const int32_t* table, int max_pages,
+                            const int32_t* start, const int32_t* n, void* k, void* v, cudaStream_t st);
+cudaError_t read_kv4_status(uint32_t* out);
+
+// Attention over the cache.  The rows of a key head, G = H / Hk query heads of
+// Nq rows each, are one dense [R = G * Nq, D] block of q and out.
+struct Kv4Plan {
+  bool tiles;   // 128-row tensor-core tiles, or a few rows per CTA
+  int nsplit;   // parts the keys of a row are split into
+};
+Kv4Plan kv4_plan(const ra_kv4_cache& c, const ra_kv4_attn& a);
+
+// Split results, joined by launch_kv4_join: per part and row an fp32 output
+// (normalised by the part's own sum) and the part's log2-sum-exp2.
+struct Kv4Parts {
+  float* o;     // [nsplit, B * Hk * R, D]
+  float* lse2;  // [nsplit, B * Hk * R]
+};
+Kv4Parts kv4_parts(const ra_kv4_cache& c, const ra_kv4_attn& a, const Kv4Plan& plan, void* ws);
+cudaError_t launch_kv4_rows(const ra_kv4_cache& c, const ra_kv4_attn& a, const Kv4Plan& plan, const void* q,
+                            const int32_t* table, const int32_t* seq_lens, const int32_t* q_lens,
+                            const Kv4Parts& parts, void* out, float* lse, cudaStream_t st);
+cudaError_t launch_kv4_join(const ra_kv4_cache& c, const ra_kv4_attn& a, const Kv4Plan& plan,
+                            const int32_t* q_lens, const Kv4Parts& parts, void* out, float* lse, cudaStream_t st);
+
+// ---------------------------------------------------------------- 128-row tiles
+cudaError_t launch_kv4_tiles(const ra_kv4_cache& c, const ra_kv4_attn& a, const Kv4Plan& plan, const void* q,
+                             const int32_t* table, const int32_t* seq_lens, const int32_t* q_lens,
+                             const Kv4Parts& parts, void* out, float* lse, cudaStream_t st);
+cudaError_t launch_attn_cross(const ra_cross_problem& p, const void* q, const ra_strides& qs, const void* k,
+                              const ra_strides& ks, const void* v, const ra_strides& vs, const int32_t* kv_lens,
+                              void* out, const ra_strides& os, float* lse, cudaStream_t st);
+cudaError_t read_tiles_status(uint32_t* out);
+
+}  // namespace ra

@@ -1,0 +1,640 @@
+// The paged 4-bit key/value cache: quantising new tokens into it, reading
+// tokens back, and attention of a few query rows per key head over it.
+// Quantisation is the INT4 rule of the prologue's Q and K (per token and head,
+// symmetric; gecl notes "Key Insight").
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "ra_common.cuh"
+#include "ra_rope.cuh"
+#include "ra_block.h"
+#include "ra_kv4.cuh"
+
+namespace ra {
+namespace {
+
+__device__ uint32_t g_kv4_status = 0;
+
+constexpr int kThreads = 256;
+
+// ---------------------------------------------------------------- append and read
+struct CacheArgs {
+  uint8_t* codes[2];      // k4, v4
+  float* scale[2];        // sk, sv
+  const void* x[2];       // append: k, v
+  void* y[2];             // read: k, v
+  ra_strides st[2];       // of x
+  const int32_t* table;
+  const int32_t* start;
+  const int32_t* count;
+  int num_pages, page_log2, max_pages, Hk, T;
+  int groups, group;      // head groups per tensor, heads per group
+};
+
+// The cache row (page * Hk * page_size + slot, head 0) of this thread's token, or -1 when the
+// token is padding or has no valid place (which is reported).
+__device__ __forceinline__ long long token_row(const CacheArgs& a, int t) {
+  const int b = blockIdx.z;
+  int cnt = a.T;
+  if (a.count) {
+    cnt = __ldg(a.count + b);
+    if (cnt < 0 || cnt > a.T) {
+      atomicOr(&g_kv4_status, kStatusBadPosition);
+      return -1;
+    }
+  }
+  if (t >= cnt) return -1;
+  const int s = a.start ? __ldg(a.start + b) : 0;
+  const long long pos = static_cast<long long>(s) + t;
+  const long long pi = pos >> a.page_log2;
+  if (s < 0 || pi >= a.max_pages) {
+    atomicOr(&g_kv4_status, kStatusBadPosition);
+    return -1;
+  }
+  const int page = __ldg(a.table + static_cast<size_t>(b) * a.max_pages + pi);
+  if (page < 0 || page >= a.num_pages) {
+    atomicOr(&g_kv4_status, kStatusBadPosition);
+    return -1;
+  }
+  return ((static_cast<long long>(page) * a.Hk) << a.page_log2) + (pos & ((1 << a.page_log2) - 1));
+}
+
+// D/8 lanes per token row, eight channels each; a thread stays with one token
+// and walks over heads, so its page is looked up once.  Bound: HBM.
+template <bool kBf16, int kD>
+__global__ void __launch_bounds__(kThreads) kv4_append_kernel(const CacheArgs a) {
+  constexpr int kLanes = kD / 8, kTok = 32 / kLanes;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int t = (blockIdx.x * (kThreads / 32) + warp) * kTok + lane / kLanes;
+  const int c0 = (lane % kLanes) * 8;
+  const int which = static_cast<int>(blockIdx.y) >= a.groups ? 1 : 0;
+  const int h0 = (blockIdx.y - (which ? a.groups : 0)) * a.group, h1 = min(h0 + a.group, a.Hk);
+  const long long row = token_row(a, t);
+  const size_t src = blockIdx.z * a.st[which].b + static_cast<size_t>(row < 0 ? 0 : t) * a.st[which].n + c0;
+#pragma unroll 4
+  for (int h = h0; h < h1; ++h) {
+    float x[8];
+    if (row >= 0) {
+      Raw8<kBf16> raw;
+      load_raw8<kBf16>(a.x[which], src + h * a.st[which].h, raw);
+      unpack8<kBf16>(raw, x);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) x[i] = 0.0f;
+    }
+    float m = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(x[i]));
+    m = group_max(m, kLanes);
+    if (m < kKv4Tiny) m = 0.0f;  // 7 / m would leave fp32's range
+    const float inv = m == 0.0f ? 0.0f : __fdiv_rn(7.0f, m);
+    uint32_t bits[8];
+#pragma unroll
+    for (int i = 0; i < 8; i += 2) quant4_bits2(x[i], x[i + 1], inv, inv, bits + i);
+    if (row >= 0) {
+      const size_t at = static_cast<size_t>(row) + (static_cast<size_t>(h) << a.page_log2);
+      *reinterpret_cast<uint32_t*>(a.codes[which] + at * (kD / 2) + (c0 >> 1)) = pack8_bits(bits);
+      if (c0 == 0) a.scale[which][at] = __fdiv_rn(m, 7.0f);
+    }
+  }
+}
+
+template <bool kBf16, int kD>
+__global__ void __launch_bounds__(kThreads) kv4_read_kernel(const CacheArgs a) {
+  constexpr int kLanes = kD / 8, kTok = 32 / kLanes;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int t = (blockIdx.x * (kThreads / 32) + warp) * kTok + lane / kLanes;
+  const int c0 = (lane % kLanes) * 8;
+  const int which = static_cast<int>(blockIdx.y) >= a.groups ? 1 : 0;
+  const int h0 = (blockIdx.y - (which ? a.groups : 0)) * a.group, h1 = min(h0 + a.group, a.Hk);
+  const long long row = token_row(a, t);
+  if (row < 0) return;
+#pragma unroll 4
+  for (int h = h0; h < h1; ++h) {
+    const size_t at = static_cast<size_t>(row) + (static_cast<size_t>(h) << a.page_log2);
+    const uint32_t w = __ldg(reinterpret_cast<const uint32_t*>(a.codes[which] + at * (kD / 2) + (c0 >> 1)));
+    const float s = __ldg(a.scale[which] + at);
+    float y[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) y[i] = static_cast<float>(static_cast<int>(w << (28 - 4 * i)) >> 28) * s;
+    const size_t o = ((static_cast<size_t>(blockIdx.z) * a.Hk + h) * a.T + t) * kD + c0;
+    if constexpr (kBf16) {
+      uint32_t p[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const __nv_bfloat162 h2 = __floats2bfloat162_rn(y[2 * i], y[2 * i + 1]);
+        p[i] = *reinterpret_cast<const uint32_t*>(&h2);
+      }
+      *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.y[which]) + o) = make_uint4(p[0], p[1], p[2], p[3]);
+    } else {
+      float4* dst = reinterpret_cast<float4*>(static_cast<float*>(a.y[which]) + o);
+      dst[0] = make_float4(y[0], y[1], y[2], y[3]);
+      dst[1] = make_float4(y[4], y[5], y[6], y[7]);
+    }
+  }
+}
+
+// ---------------------------------------------------------------- attention, few rows
+// A CTA takes up to 8 * NT query rows of one key head and one part of its
+// keys; its four warps take 32-key steps in turn, each with its own running
+// maximum, sum and output, joined at the end.  Bound: HBM, the codes and
+// scales of the keys read once ((D + 8) bytes a key and head).
+//   * Codes and scales go to shared memory by 16-byte asynchronous copies, a
+//     ring of kStages steps per warp; warps never wait for one another.
+//   * S^T = K Q^T with mma.m16n8k16: 16 keys by 8 rows, so a single query row
+//     costs half of what rows as M would.  tcgen05 (M >= 64) would spend 128
+//     rows on one.  The channels of a k step are free to choose as long as Q
+//     uses the same: a lane's 16 bytes of a key are its four words, and the
+//     nibbles j and j + 4 of a word make a bf16 pair without moving bits:
+//     (w >> 4j) & 0x000F000F, XOR 0x43084308, is the pair 128 + 8 + code,
+//     exact in bf16, and one subtraction gives the codes.
+//   * The keys' scales multiply S in fp32 and P before its one rounding to
+//     bf16, so the products see the exact codes.
+//   * O^T = V^T P^T, again 16 channels by 8 rows: P^T comes out of S^T by one
+//     8x8 transpose per 8 keys, V^T by pairing the words of two keys.  The
+//     pairs are keys x and x + 4 of each eight, which puts the rows that the
+//     lanes read at the same time into different banks.
+struct RowsArgs {
+  const uint8_t* k4;
+  const float* sk;
+  const uint8_t* v4;
+  const float* sv;
+  const __nv_bfloat16* q;
+  const int32_t* table;
+  const int32_t* seq_lens;
+  const int32_t* q_lens;
+  __nv_bfloat16* out;
+  float* lse;
+  Kv4Parts parts;
+  int num_pages, page_log2, max_pages, Hk, G, Nq, causal, nsplit;
+  float scale_log2;  // scale * log2(e)
+};
+
+constexpr int kRowWarps = 4;
+constexpr int kStep = 32;    // keys per warp and step
+constexpr int kStages = 3;
+constexpr float kLazy = 8.0f;  // the reference maximum moves when a score passes it by this (powers of two)
+
+template <int D>
+struct RowsCfg {
+  static constexpr int kRow = D / 2;                    // code bytes of a key
+  static constexpr int kChunks = kRow / 16;             // 16-byte chunks of a key
+  static constexpr int oV = kStep * kRow;
+  static constexpr int oSk = 2 * kStep * kRow;
+  static constexpr int oSv = oSk + kStep * 4;
+  static constexpr int kStage = oSv + kStep * 4;
+  static constexpr int kSmem = kRowWarps * kStages * kStage;
+};
+
+// Place of key x (0..15) of a 16-key group in the K tile, which the lanes of
+// row group g read at places g and 8 + g: keys 8j + g/2 (g even) or 8j + 4 + g/2.
+__device__ __forceinline__ int k_place(int x) { return (x & 8) | ((x & 3) << 1) | ((x >> 2) & 1); }
+// Key of place g of eight.
+__device__ __forceinline__ int key_of(int g) { return (g >> 1) | ((g & 1) << 2); }
+
+template <int D, int NT>
+__global__ void __launch_bounds__(kRowWarps * 32) kv4_rows_kernel(const RowsArgs a) {
+  using C = RowsCfg<D>;
+  constexpr int kW = D / 32;        // code words of a key per lane (K)
+  constexpr int kM = D / 16;        // 16-channel tiles of the output
+  extern __shared__ __align__(128) uint8_t smem[];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int g = lane >> 2, q4 = lane & 3;
+  const int bh = blockIdx.z, b = bh / a.Hk, hk = bh % a.Hk;
+  const int split = blockIdx.x, r0 = blockIdx.y * 8 * NT;
+  const int R = a.G * a.Nq;
+  uint32_t bad = 0;
+  const int len = clamp_len(__ldg(a.seq_lens + b), a.max_pages << a.page_log2, &bad);
+  const int ql = a.q_lens ? clamp_len(__ldg(a.q_lens + b), a.Nq, &bad) : a.Nq;
+  // Steps of this CTA: [t0, t1), every kRowWarps-th for this warp.
+  const int nstep = (len + kStep - 1) / kStep;
+  const int per = (nstep + a.nsplit - 1) / a.nsplit;
+  const int t0 = min(split * per, nstep), t1 = min(t0 + per, nstep);
+
+  uint8_t* const ring = smem + warp * kStages * C::kStage;
+  auto load = [&](int t, int stage) {
+    uint8_t* const st = ring + stage * C::kStage;
+    const int32_t* const tb = a.table + static_cast<size_t>(b) * a.max_pages;
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+      const int key0 = t * kStep + 16 * s;
+      const bool live = t < t1 && key0 < len;
+      size_t row = 0;
+      if (live) {
+        int page = __ldg(tb + (key0 >> a.page_log2));
+        if (page < 0 || page >= a.num_pages) {
+          bad |= kStatusBadPosition;
+          page = 0;
+        }
+        row = ((static_cast<size_t>(page) * a.Hk + hk) << a.page_log2) + (key0 & ((1 << a.page_log2) - 1));
+      }
+      const uint32_t bytes = live ? 16u : 0u;  // 0: the place is filled with zeros
+#pragma unroll
+      for (int i = 0; i < 16 * C::kChunks / 32; ++i) {
+        const int idx = lane + 32 * i, x = idx / C::kChunks, ch = idx % C::kChunks;
+        cp_async16(st + (16 * s + k_place(x)) * C::kRow + ch * 16, a.k4 + (row + x) * C::kRow + ch * 16, bytes);
+        const int vch = C::kChunks == 4 ? ch ^ (x & 2) : ch;
+        cp_async16(st + C::oV + (16 * s + x) * C::kRow + vch * 16, a.v4 + (row + x) * C::kRow + ch * 16, bytes);
+      }
+      if (lane < 8) {
+        const float* const src = lane < 4 ? a.sk : a.sv;
+        cp_async16(st + (lane < 4 ? C::oSk : C::oSv) + 64 * s + (lane & 3) * 16, src + row + (lane & 3) * 4, bytes);
+      }
+    }
+    cp_async_commit();
+  };
+#pragma unroll
+  for (int i = 0; i < kStages - 1; ++i) load(t0 + warp + i * kRowWarps, i);
+
+  // Q fragments: row 8j + g, the channels of this lane's words.
+  uint32_t qf[NT][2 * kW][2];
+  int lim[NT][2];
+  int lim_min = len;
+#pragma unroll
+  for (int j = 0; j < NT; ++j) {
+    const int r = r0 + 8 * j + g;
+    const bool ok = r < R && r % a.Nq < ql;
+    const __nv_bfloat16* const src = a.q + (static_cast<size_t>(bh) * R + (ok ? r : 0)) * D + q4 * (D / 4);
+#pragma unroll
+    for (int w = 0; w < kW; ++w) {
+      const uint4 u = ok ? __ldg(reinterpret_cast<const uint4*>(src + 8 * w)) : make_uint4(0, 0, 0, 0);
+      qf[j][2 * w][0] = __byte_perm(u.x, u.z, 0x5410);      // channels 0, 4
+      qf[j][2 * w][1] = __byte_perm(u.x, u.z, 0x7632);      // 1, 5
+      qf[j][2 * w + 1][0] = __byte_perm(u.y, u.w, 0x5410);  // 2, 6
+      qf[j][2 * w + 1][1] = __byte_perm(u.y, u.w, 0x7632);  // 3, 7
+    }
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int rr = r0 + 8 * j + 2 * q4 + e, i = rr % a.Nq;
+      lim[j][e] = rr < R && i < ql ? (a.causal ? max(len - ql + i + 1, 0) : len) : 0;
+    }
+  }
+  if (a.causal) lim_min = max(len - a.Nq, 0);
+
+  float acc[NT][kM][4];
+  float m[NT][2], l[NT][2];
+#pragma unroll
+  for (int j = 0; j < NT; ++j) {
+#pragma unroll
+    for (int i = 0; i < kM; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) acc[j][i][e] = 0.0f;
+    m[j][0] = m[j][1] = -INFINITY;
+    l[j][0] = l[j][1] = 0.0f;
+  }
+  int stage = 0;
+  for (int t = t0 + warp; t < t1; t += kRowWarps) {
+    cp_async_wait<kStages - 2>();
+    __syncwarp();
+    {
+      int ns = stage + kStages - 1;
+      if (ns >= kStages) ns -= kStages;
+      load(t + (kStages - 1) * kRowWarps, ns);
+    }
+    const uint8_t* const st = ring + stage * C::kStage;
+    if (++stage == kStages) stage = 0;
+    // ---- S^T of 2 x 16 keys
+    float s[NT][2][4];
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      uint32_t w0[kW], w1[kW];
+      load_words<kW>(st + (16 * u + g) * C::kRow + q4 * (C::kRow / 4), w0);
+      load_words<kW>(st + (16 * u + 8 + g) * C::kRow + q4 * (C::kRow / 4), w1);
+#pragma unroll
+      for (int j = 0; j < NT; ++j) s[j][u][0] = s[j][u][1] = s[j][u][2] = s[j][u][3] = 0.0f;
+#pragma unroll
+      for (int w = 0; w < kW; ++w)
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          uint32_t af[4];
+          af[0] = codes_bf16(w0[w] >> (8 * k));
+          af[1] = codes_bf16(w1[w] >> (8 * k));
+          af[2] = codes_bf16(w0[w] >> (8 * k + 4));
+          af[3] = codes_bf16(w1[w] >> (8 * k + 4));
+#pragma unroll
+          for (int j = 0; j < NT; ++j) mma_bf16(s[j][u], af, qf[j][2 * w + k][0], qf[j][2 * w + k][1]);
+        }
+    }
+    // ---- scores in powers of two, masked; the reference maximum
+    const float* const skp = reinterpret_cast<const float*>(st + C::oSk) + key_of(g);
+    const float* const svp = reinterpret_cast<const float*>(st + C::oSv) + key_of(g);
+    const int kbase = t * kStep + key_of(g);
+    const bool edge = t * kStep + kStep > lim_min;
+    bool up = false;
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const float f = skp[16 * u + 8 * e] * a.scale_log2;
+        const int key = kbase + 16 * u + 8 * e;
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+#pragma unroll
+          for (int n = 0; n < 2; ++n) {
+            float& y = s[j][u][2 * e + n];
+            y *= f;
+            if (edge && key >= lim[j][n]) y = -INFINITY;
+            up |= y > m[j][n] + kLazy;
+          }
+      }
+    if (__any_sync(0xFFFFFFFFu, up)) {
+#pragma unroll
+      for (int j = 0; j < NT; ++j) {
+        float f[2];
+#pragma unroll
+        for (int n = 0; n < 2; ++n) {
+          float x = fmaxf(fmaxf(s[j][0][n], s[j][0][2 + n]), fmaxf(s[j][1][n], s[j][1][2 + n]));
+#pragma unroll
+          for (int o = 4; o < 32; o <<= 1) x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, o));
+          const float mn = fmaxf(m[j][n], x);
+          f[n] = mn == -INFINITY ? 1.0f : ex2_approx(m[j][n] - mn);
+          m[j][n] = mn;
+          l[j][n] *= f[n];
+        }
+#pragma unroll
+        for (int i = 0; i < kM; ++i) {
+          acc[j][i][0] *= f[0];
+          acc[j][i][1] *= f[1];
+          acc[j][i][2] *= f[0];
+          acc[j][i][3] *= f[1];
+        }
+      }
+    }
+    // ---- P^T (times the values' scales) and O^T
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      uint32_t pb[NT][2];
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        // Slots behind the last key may hold anything: 0 * NaN is not 0.
+        const float fv = kbase + 16 * u + 8 * e < len ? svp[16 * u + 8 * e] : 0.0f;
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+          float p[2];
+#pragma unroll
+          for (int n = 0; n < 2; ++n) {
+            const float mr = m[j][n] == -INFINITY ? 0.0f : m[j][n];
+            p[n] = ex2_approx(s[j][u][2 * e + n] - mr);
+            l[j][n] += p[n];
+          }
+          pb[j][e] = transpose8(pack_bf16(p[0] * fv, p[1] * fv));
+        }
+      }
+      constexpr int kVW = D / 64;  // code words of a key per lane (V)
+      uint32_t x[4][kVW];          // keys q4, q4 + 4, 8 + q4, 12 + q4
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int r = 16 * u + 4 * i + q4;
+        const int ch = kVW == 2 ? ((g >> 1) ^ (r & 2)) * 16 + (g & 1) * 8 : g * 4;
+        load_words<kVW>(st + C::oV + r * C::kRow + ch, x[i]);
+      }
+      // Channels of this lane: its words' nibbles in order; tile i has nibble i
+      // of the first half of them as row g and of the second as row g + 8.
+#pragma unroll
+      for (int i = 0; i < kM; ++i) {
+        uint32_t af[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int nib = i + (e & 1) * kM;              // 0 .. D/8 - 1
+          const int w = nib >> 3, half = (nib >> 2) & 1, sh = 4 * (nib & 3);
+          const uint32_t x0 = x[(e >> 1) * 2][w], x1 = x[(e >> 1) * 2 + 1][w];
+          af[e] = codes_bf16(__byte_perm(x0, x1, half ? 0x7632 : 0x5410) >> sh);
+        }
+#pragma unroll
+        for (int j = 0; j < NT; ++j) mma_bf16(acc[j][i], af, pb[j][0], pb[j][1]);
+      }
+    }
+  }
+  cp_async_wait<0>();
+  if (bad) atomicOr(&g_kv4_status, bad);
+
+  // ---- join the warps' results
+#pragma unroll
+  for (int j = 0; j < NT; ++j)
+#pragma unroll
+    for (int n = 0; n < 2; ++n)
+#pragma unroll
+      for (int o = 4; o < 32; o <<= 1) l[j][n] += __shfl_xor_sync(0xFFFFFFFFu, l[j][n], o);
+  __syncthreads();
+  constexpr int kRows = 8 * NT;
+  float* const ro = reinterpret_cast<float*>(smem);                 // [warp][row][D]
+  float* const rm = ro + kRowWarps * kRows * D;                     // [warp][row]
+  float* const rl = rm + kRowWarps * kRows;
+  static_assert((kRowWarps * kRows * (D + 2)) * 4 <= C::kSmem, "shared memory of the join");
+#pragma unroll
+  for (int j = 0; j < NT; ++j) {
+#pragma unroll
+    for (int i = 0; i < kM; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        ro[(warp * kRows + 8 * j + 2 * q4 + (e & 1)) * D + g * (D / 8) + i + (e >> 1) * kM] = acc[j][i][e];
+    if (g == 0) {
+#pragma unroll
+      for (int n = 0; n < 2; ++n) {
+        rm[warp * kRows + 8 * j + 2 * q4 + n] = m[j][n];
+        rl[warp * kRows + 8 * j + 2 * q4 + n] = l[j][n];
+      }
+    }
+  }
+  __syncthreads();
+  for (int idx = threadIdx.x; idx < kRows * (D / 4); idx += kRowWarps * 32) {
+    const int row = idx / (D / 4), c = (idx % (D / 4)) * 4;
+    const int r = r0 + row;
+    if (r >= R || r % a.Nq >= ql) continue;
+    float top = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < kRowWarps; ++w) top = fmaxf(top, rm[w * kRows + row]);
+    float sum = 0.0f;
+    float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+    for (int w = 0; w < kRowWarps; ++w) {
+      const float mw = rm[w * kRows + row];
+      const float f = mw == -INFINITY ? 0.0f : ex2_approx(mw - top);
+      const float4 v = *reinterpret_cast<const float4*>(ro + (w * kRows + row) * D + c);
+      sum = fmaf(f, rl[w * kRows + row], sum);
+      o.x = fmaf(f, v.x, o.x); o.y = fmaf(f, v.y, o.y); o.z = fmaf(f, v.z, o.z); o.w = fmaf(f, v.w, o.w);
+    }
+    const float inv = top == -INFINITY ? 0.0f : 1.0f / sum;
+    const float lse2 = top == -INFINITY ? -INFINITY : top + log2f(sum);
+    const size_t at = static_cast<size_t>(bh) * R + r;
+    o.x *= inv; o.y *= inv; o.z *= inv; o.w *= inv;
+    if (a.nsplit == 1) {
+      *reinterpret_cast<uint2*>(a.out + at * D + c) = make_uint2(pack_bf16(o.x, o.y), pack_bf16(o.z, o.w));
+      if (c == 0 && a.lse) a.lse[at] = lse2 * kLn2;
+    } else {
+      const size_t pr = static_cast<size_t>(split) * gridDim.z * R + at;
+      *reinterpret_cast<float4*>(a.parts.o + pr * D + c) = o;
+      if (c == 0) a.parts.lse2[pr] = lse2;
+    }
+  }
+}
+
+// Joins the parts of every row, one warp per row: weights 2^(lse2 - max).
+template <int D>
+__global__ void __launch_bounds__(128) kv4_join_kernel(Kv4Parts parts, int nsplit, long long rows, int Nq, int rows_b,
+                                                       const int32_t* q_lens, __nv_bfloat16* out, float* lse) {
+  constexpr int kC = D / 32;
+  const int lane = threadIdx.x & 31;
+  const long long r = static_cast<long long>(blockIdx.x) * 4 + (threadIdx.x >> 5);
+  if (r >= rows) return;
+  if (q_lens && static_cast<int>(r % Nq) >= __ldg(q_lens + r / rows_b)) return;
+  float top = -INFINITY;
+  for (int s = 0; s < nsplit; ++s) top = fmaxf(top, parts.lse2[s * rows + r]);
+  float sum = 0.0f, o[kC];
+#pragma unroll
+  for (int i = 0; i < kC; ++i) o[i] = 0.0f;
+#pragma unroll 4
+  for (int s = 0; s < nsplit; ++s) {
+    const float x = parts.lse2[s * rows + r];
+    const float w = x == -INFINITY ? 0.0f : ex2_approx(x - top);
+    sum += w;
+    const float* src = parts.o + (s * rows + r) * D + lane * kC;
+#pragma unroll
+    for (int i = 0; i < kC; i += 2) {
+      const float2 v = *reinterpret_cast<const float2*>(src + i);
+      o[i] = fmaf(w, v.x, o[i]);
+      o[i + 1] = fmaf(w, v.y, o[i + 1]);
+    }
+  }
+  const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
+  uint32_t* dst = reinterpret_cast<uint32_t*>(out + r * D + lane * kC);
+#pragma unroll
+  for (int i = 0; i < kC; i += 2) dst[i / 2] = pack_bf16(o[i] * inv, o[i + 1] * inv);
+  if (lse && lane == 0) lse[r] = sum > 0.0f ? (top + log2f(sum)) * kLn2 : -INFINITY;
+}
+
+int log2_of(int x) { return __builtin_ctz(static_cast<unsigned>(x)); }
+
+CacheArgs cache_args(const ra_kv4_cache& c, int B, int T, const int32_t* table, int max_pages, const int32_t* start,
+                     const int32_t* count, dim3* grid) {
+  CacheArgs a{};
+  a.codes[0] = c.k4; a.codes[1] = c.v4;
+  a.scale[0] = c.sk; a.scale[1] = c.sv;
+  a.table = table; a.start = start; a.count = count;
+  a.num_pages = c.num_pages; a.page_log2 = log2_of(c.page_size); a.max_pages = max_pages;
+  a.Hk = c.Hk; a.T = T;
+  const int tok = (kThreads / 32) * (256 / c.D);
+  const int tiles = (T + tok - 1) / tok;
+  int group = 8;  // heads per CTA: as many as leave eight CTAs per SM, at most eight
+  while (group > 1 && static_cast<long long>(tiles) * B * 2 * ((c.Hk + group - 1) / group) < 8LL * kNumSMs) group >>= 1;
+  a.group = group;
+  a.groups = (c.Hk + group - 1) / group;
+  *grid = dim3(tiles, 2 * a.groups, B);
+  return a;
+}
+
+template <int D, int NT>
+cudaError_t launch_rows(const RowsArgs& a, dim3 grid, cudaStream_t st) {
+  auto kern = kv4_rows_kernel<D, NT>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, RowsCfg<D>::kSmem);
+  if (e != cudaSuccess) return e;
+  kern<<<grid, kRowWarps * 32, RowsCfg<D>::kSmem, st>>>(a);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_kv4_append(const ra_kv4_cache& c, int dtype, int B, int T, const void* k, const ra_strides& ks,
+                              const void* v, const ra_strides& vs, const int32_t* table, int max_pages,
+                              const int32_t* start, const int32_t* n_new, cudaStream_t st) {
+  dim3 grid;
+  CacheArgs a = cache_args(c, B, T, table, max_pages, start, n_new, &grid);
+  a.x[0] = k; a.x[1] = v;
+  a.st[0] = ks; a.st[1] = vs;
+  if (dtype == RA_DT_BF16) {
+    if (c.D == 64) kv4_append_kernel<true, 64><<<grid, kThreads, 0, st>>>(a);
+    else kv4_append_kernel<true, 128><<<grid, kThreads, 0, st>>>(a);
+  } else {
+    if (c.D == 64) kv4_append_kernel<false, 64><<<grid, kThreads, 0, st>>>(a);
+    else kv4_append_kernel<false, 128><<<grid, kThreads, 0, st>>>(a);
+  }
+  return cudaGetLastError();
+}
+
+cudaError_t launch_kv4_read(const ra_kv4_cache& c, int dtype, int B, int T, const int32_t* table, int max_pages,
+                            const int32_t* start, const int32_t* n, void* k, void* v, cudaStream_t st) {
+  dim3 grid;
+  CacheArgs a = cache_args(c, B, T, table, max_pages, start, n, &grid);
+  a.y[0] = k; a.y[1] = v;
+  if (dtype == RA_DT_BF16) {
+    if (c.D == 64) kv4_read_kernel<true, 64><<<grid, kThreads, 0, st>>>(a);
+    else kv4_read_kernel<true, 128><<<grid, kThreads, 0, st>>>(a);
+  } else {
+    if (c.D == 64) kv4_read_kernel<false, 64><<<grid, kThreads, 0, st>>>(a);
+    else kv4_read_kernel<false, 128><<<grid, kThreads, 0, st>>>(a);
+  }
+  return cudaGetLastError();
+}
+
+Kv4Plan kv4_plan(const ra_kv4_cache& c, const ra_kv4_attn& a) {
+  Kv4Plan plan{};
+  const long long R = static_cast<long long>(a.H / c.Hk) * a.Nq, bh = static_cast<long long>(a.B) * c.Hk;
+  plan.tiles = R > 16;
+  const long long slots = plan.tiles ? kNumSMs : 4 * kNumSMs;
+  const long long items = bh * (plan.tiles ? (R + 255) / 256 : 1);
+  const int keys = plan.tiles ? 512 : 128;  // a part has at least this many keys
+  const int most = a.max_len < keys ? 1 : a.max_len / keys;
+  // The smallest number of parts whose last wave of CTAs is nearly full.
+  int best = 1;
+  double best_fill = 0.0;
+  for (int k = 1; k <= most && k <= 64; ++k) {
+    const long long n = items * k;
+    const double fill = static_cast<double>(n) / static_cast<double>((n + slots - 1) / slots * slots);
+    if (fill > best_fill + 0.02) {
+      best = k;
+      best_fill = fill;
+    }
+    if (fill >= 0.9) break;
+  }
+  plan.nsplit = best;
+  return plan;
+}
+
+Kv4Parts kv4_parts(const ra_kv4_cache& c, const ra_kv4_attn& a, const Kv4Plan& plan, void* ws) {
+  Kv4Parts p{};
+  if (plan.nsplit == 1) return p;
+  const size_t rows = static_cast<size_t>(a.B) * a.H * a.Nq;
+  p.o = static_cast<float*>(ws);
+  p.lse2 = p.o + plan.nsplit * rows * c.D;
+  return p;
+}
+
+cudaError_t launch_kv4_rows(const ra_kv4_cache& c, const ra_kv4_attn& at, const Kv4Plan& plan, const void* q,
+                            const int32_t* table, const int32_t* seq_lens, const int32_t* q_lens,
+                            const Kv4Parts& parts, void* out, float* lse, cudaStream_t st) {
+  RowsArgs a{};
+  a.k4 = c.k4; a.sk = c.sk; a.v4 = c.v4; a.sv = c.sv;
+  a.q = static_cast<const __nv_bfloat16*>(q);
+  a.table = table; a.seq_lens = seq_lens; a.q_lens = q_lens;
+  a.out = static_cast<__nv_bfloat16*>(out);
+  a.lse = lse;
+  a.parts = parts;
+  a.num_pages = c.num_pages; a.page_log2 = log2_of(c.page_size); a.max_pages = at.max_pages;
+  a.Hk = c.Hk; a.G = at.H / c.Hk; a.Nq = at.Nq; a.causal = at.causal; a.nsplit = plan.nsplit;
+  a.scale_log2 = at.scale * kLog2e;
+  const int R = a.G * a.Nq;
+  const dim3 grid(plan.nsplit, (R + 15) / 16, at.B * c.Hk);
+  if (R <= 8) return c.D == 64 ? launch_rows<64, 1>(a, grid, st) : launch_rows<128, 1>(a, grid, st);
+  return c.D == 64 ? launch_rows<64, 2>(a, grid, st) : launch_rows<128, 2>(a, grid, st);
+}
+
+cudaError_t launch_kv4_join(const ra_kv4_cache& c, const ra_kv4_attn& a, const Kv4Plan& plan,
+                            const int32_t* q_lens, const Kv4Parts& parts, void* out, float* lse, cudaStream_t st) {
+  const long long rows = static_cast<long long>(a.B) * a.H * a.Nq;
+  const int grid = static_cast<int>((rows + 3) / 4), rows_b = a.H * a.Nq;
+  __nv_bfloat16* o = static_cast<__nv_bfloat16*>(out);
+  if (c.D == 64) kv4_join_kernel<64><<<grid, 128, 0, st>>>(parts, plan.nsplit, rows, a.Nq, rows_b, q_lens, o, lse);
+  else kv4_join_kernel<128><<<grid, 128, 0, st>>>(parts, plan.nsplit, rows, a.Nq, rows_b, q_lens, o, lse);
+  return cudaGetLastError();
+}
+
+cudaError_t read_kv4_status(uint32_t* out) {
+  uint32_t zero = 0;
+  cudaError_t e = cudaMemcpyFromSymbol(out, g_kv4_status, sizeof(uint32_t));
+  if (e != cudaSuccess) return e;
+  return cudaMemcpyToSymbol(g_kv4_status, &zero, sizeof(uint32_t));
+}
+
+}  // namespace ra

@@ -1,0 +1,78 @@
+// Device helpers of the 4-bit key/value cache: code unpacking, mma.sync and
+// asynchronous 16-byte copies.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "ra_common.cuh"
+
+namespace ra {
+
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+constexpr float kKv4Tiny = 2.350988701644575e-38f;  // 2^-125: rows below it are stored as zeros
+
+// A length given by the caller, held to [0, most]; a value outside is noted.
+__device__ __forceinline__ int clamp_len(int x, int most, uint32_t* bad) {
+  if (x < 0 || x > most) *bad |= kStatusBadPosition;
+  return min(max(x, 0), most);
+}
+
+// The two codes in bits 0-3 and 16-19 of w as a bf16 pair: two's complement
+// XOR 8 is code + 8, in the low bits of a bf16 of exponent 7 it is 128 + 8 +
+// code, and the subtraction of 136 is exact.
+__device__ __forceinline__ uint32_t codes_bf16(uint32_t w) {
+  const uint32_t x = (w & 0x000F000Fu) ^ 0x43084308u;
+  const uint32_t k136 = 0x43084308u;  // 136 as bf16, twice
+  const __nv_bfloat162 r = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&x),
+                                   *reinterpret_cast<const __nv_bfloat162*>(&k136));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// N words from shared memory (aligned to their size) as one access.
+template <int N>
+__device__ __forceinline__ void load_words(const uint8_t* p, uint32_t* w) {
+  if constexpr (N == 1) {
+    w[0] = *reinterpret_cast<const uint32_t*>(p);
+  } else if constexpr (N == 2) {
+    const uint2 v = *reinterpret_cast<const uint2*>(p);
+    w[0] = v.x; w[1] = v.y;
+  } else {
+    const uint4 v = *reinterpret_cast<const uint4*>(p);
+    w[0] = v.x; w[1] = v.y; w[2] = v.z; w[3] = v.w;
+  }
+}
+
+// c += a b, bf16 in, fp32 out: a 16 x 16 (row), b 16 x 8 (column).
+__device__ __forceinline__ void mma_bf16(float* c, const uint32_t* a, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// Transposes the warp's 8 x 8 matrix of 16-bit values.
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+
+// 16 bytes global -> shared without registers; `bytes` 0 fills with zeros.
+__device__ __forceinline__ void cp_async16(void* dst, const void* src, uint32_t bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+}  // namespace ra

@@ -1,0 +1,174 @@
+// Norm of every head's query and key row, 3D RoPE and the RoPE-aware rotation
+// in one pass (papernotes page, key design 1: R M q and R M k; the norms are
+// the q/k norms of the video transformers the method is applied to).
+//
+// For each row x of D channels, in fp32:
+//   y = (x - mu) * rsqrt(mean((x - mu)^2) + eps) * w + b   (mu = 0 for RMS)
+//   then the pair products with the RoPE table and the rotation of ra_rope.cuh,
+//   rounded once to bf16.
+//
+// Bound: HBM (read each row once, write it once; about 10 operations a channel).
+// D/8 lanes hold a row, eight channels each, so a row is one or two 16-byte
+// loads per lane and its sums are four or three shuffles.  A thread stays with
+// one token and walks over heads: positions and table entries are loaded once
+// for all of them, and in token-major projections the heads of a token are
+// neighbours in memory.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "ra_common.cuh"
+#include "ra_rope.cuh"
+#include "ra_block.h"
+
+namespace ra {
+namespace {
+
+__device__ uint32_t g_norm_status = 0;
+
+constexpr int kThreads = 256;
+
+struct NormArgs {
+  const void* x[2];
+  ra_strides st[2];
+  const float* weight[2];
+  const float* bias[2];
+  __nv_bfloat16* out[2];
+  int heads[2];
+  int groups_q;      // head groups of q; the groups of k follow
+  int group;         // heads per group
+  int N;
+  float eps;
+  const int32_t* pos;
+  const float2* tab;
+  SegInfo s;
+};
+
+__device__ __forceinline__ float group_sum(float v, int lpt) {
+  for (int o = lpt >> 1; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+  return v;
+}
+
+// kRot: the rotation, or -1 for the norm alone.
+template <bool kBf16, int kD, int kRot, bool kLayer>
+__global__ void __launch_bounds__(kThreads) norm_rope_kernel(const NormArgs a) {
+  constexpr int kLanes = kD / 8, kTok = 32 / kLanes;  // lanes per row, tokens per warp
+  __shared__ float rows[kRot == RA_ROT_HALF ? kThreads / 32 : 1][kTok][kD];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int tok = lane / kLanes, c0 = (lane % kLanes) * 8;
+  const int which = static_cast<int>(blockIdx.y) >= a.groups_q ? 1 : 0;
+  const int h0 = (blockIdx.y - (which ? a.groups_q : 0)) * a.group;
+  const int h1 = min(h0 + a.group, a.heads[which]);
+  const int n = (blockIdx.x * (kThreads / 32) + warp) * kTok + tok;
+  const bool in_range = n < a.N;
+  const int nc = in_range ? n : a.N - 1;  // lanes past the end work on the last row and do not store
+  RopePlan rp;
+  float2 cf[4];
+  if constexpr (kRot >= 0) {
+    rp.init(a.s, c0);
+    int gp[3];
+#pragma unroll
+    for (int j = 0; j < 3; ++j) gp[j] = __ldg(a.pos + 3 * nc + j);
+    rope_coef8p(a.s, rp, a.tab, gp, cf, &g_norm_status);
+  }
+  float w[8], b[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    w[i] = a.weight[which] ? __ldg(a.weight[which] + c0 + i) : 1.0f;
+    b[i] = a.bias[which] ? __ldg(a.bias[which] + c0 + i) : 0.0f;
+  }
+  const size_t src = blockIdx.z * a.st[which].b + nc * a.st[which].n + c0;
+  const size_t hn = static_cast<size_t>(a.N) * kD;
+  __nv_bfloat16* dst = a.out[which] + blockIdx.z * hn * a.heads[which] + static_cast<size_t>(nc) * kD + c0;
+#pragma unroll 4
+  for (int h = h0; h < h1; ++h) {
+    Raw8<kBf16> raw;
+    load_raw8<kBf16>(a.x[which], src + h * a.st[which].h, raw);
+    float x[8];
+    unpack8<kBf16>(raw, x);
+    if constexpr (kLayer) {
+      float s = 0.0f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) s += x[i];
+      const float mu = group_sum(s, kLanes) * (1.0f / kD);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) x[i] -= mu;
+    }
+    float ss = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) ss = fmaf(x[i], x[i], ss);
+    const float r = rsqrtf(fmaf(group_sum(ss, kLanes), 1.0f / kD, a.eps));
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = fmaf(x[i] * r, w[i], b[i]);
+    if constexpr (kRot >= 0) rope_apply8(a.s, rp, kRot, cf, c0, x, rows[kRot == RA_ROT_HALF ? warp : 0][tok]);
+    uint32_t o[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const __nv_bfloat162 h2 = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
+      o[i] = *reinterpret_cast<const uint32_t*>(&h2);
+    }
+    if (in_range) *reinterpret_cast<uint4*>(dst + h * hn) = make_uint4(o[0], o[1], o[2], o[3]);
+  }
+}
+
+template <bool kBf16, int kD, int kRot>
+cudaError_t launch_norm(const NormArgs& a, bool layer, dim3 grid, cudaStream_t st) {
+  if (layer) norm_rope_kernel<kBf16, kD, kRot, true><<<grid, kThreads, 0, st>>>(a);
+  else norm_rope_kernel<kBf16, kD, kRot, false><<<grid, kThreads, 0, st>>>(a);
+  return cudaGetLastError();
+}
+
+template <bool kBf16, int kD>
+cudaError_t launch_rot(const NormArgs& a, int rot, bool layer, dim3 grid, cudaStream_t st) {
+  switch (rot) {
+    case RA_ROT_NONE: return launch_norm<kBf16, kD, RA_ROT_NONE>(a, layer, grid, st);
+    case RA_ROT_INTERLEAVED: return launch_norm<kBf16, kD, RA_ROT_INTERLEAVED>(a, layer, grid, st);
+    case RA_ROT_HALF: return launch_norm<kBf16, kD, RA_ROT_HALF>(a, layer, grid, st);
+    case RA_ROT_FULL: return launch_norm<kBf16, kD, RA_ROT_FULL>(a, layer, grid, st);
+    default: return launch_norm<kBf16, kD, -1>(a, layer, grid, st);
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_norm_rope(const ra_problem& p, const NormRopeCall& c, cudaStream_t st) {
+  NormArgs a{};
+  int heads = 0;
+  for (int i = 0; i < 2; ++i) {
+    a.x[i] = c.x[i];
+    a.st[i] = c.st[i];
+    a.weight[i] = c.weight[i];
+    a.bias[i] = c.bias[i];
+    a.out[i] = static_cast<__nv_bfloat16*>(c.out[i]);
+    a.heads[i] = c.x[i] ? c.heads[i] : 0;
+    heads += a.heads[i];
+  }
+  a.N = p.N;
+  a.eps = c.eps;
+  a.pos = c.pos;
+  a.tab = c.tab;
+  a.s = seg_info(p);
+  const int tok = (kThreads / 32) * (256 / p.D);  // tokens per CTA
+  const int tiles = (p.N + tok - 1) / tok;
+  // Heads per CTA: as many as leave eight CTAs per SM, at most eight.
+  int group = 8;
+  while (group > 1 && static_cast<long long>(tiles) * p.B * ((heads + group - 1) / group) < 8LL * kNumSMs) group >>= 1;
+  a.group = group;
+  a.groups_q = (a.heads[0] + group - 1) / group;
+  const dim3 grid(tiles, a.groups_q + (a.heads[1] + group - 1) / group, p.B);
+  const int rot = c.pos ? p.rot : -1;
+  const bool layer = c.norm == RA_NORM_LAYER;
+  if (c.dtype == RA_DT_BF16)
+    return p.D == 64 ? launch_rot<true, 64>(a, rot, layer, grid, st) : launch_rot<true, 128>(a, rot, layer, grid, st);
+  return p.D == 64 ? launch_rot<false, 64>(a, rot, layer, grid, st) : launch_rot<false, 128>(a, rot, layer, grid, st);
+}
+
+cudaError_t read_norm_rope_status(uint32_t* out) {
+  uint32_t zero = 0;
+  cudaError_t e = cudaMemcpyFromSymbol(out, g_norm_status, sizeof(uint32_t));
+  if (e != cudaSuccess) return e;
+  return cudaMemcpyToSymbol(g_norm_status, &zero, sizeof(uint32_t));
+}
+
+}  // namespace ra
