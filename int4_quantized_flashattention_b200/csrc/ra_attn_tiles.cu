@@ -3,20 +3,21 @@
 //   O = softmax(scale q k^T) v, fp32 scores, softmax and sums.
 //
 // One persistent CTA per SM takes two 128-row query tiles of one head (an
-// item) and walks over 128-key blocks; the two tiles share each block and
-// alternate on the tensor cores, one's products running under the other's
-// softmax.
+// item) and walks over 64-key blocks, which the tiles share.  S has two buffers
+// per tile, so the tensor cores work on one block while the softmax is at the
+// other: with 128-key blocks and one buffer a tile's products and its softmax
+// took turns (890 TFLOP/s at 8192 x 8192, D = 128, softmax warps idle half of
+// the time).
 //   warp 0      TMA producer: Q, and (cross) K and V, 64-channel boxes with the
 //               128-byte swizzle
 //   warps 1, 2  MMA issuers of tiles 0 and 1: S = Q K^T into TMEM (tcgen05
-//               kind::f16, M = N = 128), then O += P V with P read from TMEM
+//               kind::f16, M = 128, N = 64), then O += P V with P read from TMEM
 //   warp 3      (cross) clears value rows behind the last key, which may hold
 //               anything, before the MMA reads them: 0 * NaN is not 0
 //   warps 4-7   (cache) unpack codes into bf16 K and V tiles (exact); a thread
 //               per key, the next block's codes in flight in its registers
 //   then 4 + 4  softmax warps, one row per thread: no exchange between threads.
-// P overwrites the S columns it came from, so the next S of the tile follows
-// P V.  The reference maximum moves only when a score passes it by 2^8
+// P overwrites the S columns it came from.  The reference maximum moves only when a score passes it by 2^8
 // (kLazy): rescaling O in TMEM is rare, and P stays below 2^8, which bf16
 // holds as well as 1.  The scales of the cache multiply the scores (keys) and
 // P before its rounding (values) in fp32.
@@ -39,21 +40,24 @@ __device__ uint32_t g_tiles_status = 0;
 
 constexpr int kRows = 128;   // query rows per tile = MMA M
 constexpr int kTiles = 2;    // query tiles per CTA
-constexpr int kKeys = 128;   // keys per block = MMA N of S
+constexpr int kKeys = 64;    // keys per block = MMA N of S
 constexpr float kLazy = 8.0f;
 
 template <int D, bool KV4>
 struct CfgT {
   static constexpr int kHalves = D / 64;
-  static constexpr int kHalf = kRows * 128;            // one 64-channel box of 128 rows
-  static constexpr int kTileBytes = kRows * D * 2;     // a Q, K or V tile
-  static constexpr int kStages = 2;                    // of K, and of V
+  static constexpr int kQHalf = kRows * 128;           // a 64-channel box of a Q tile
+  static constexpr int kHalf = kKeys * 128;            // and of a K or V block
+  static constexpr int kQBytes = kRows * D * 2;
+  static constexpr int kKVBytes = kKeys * D * 2;
+  static constexpr int kStages = 4;                    // of K, and of V
   static constexpr int oQ = 0;
-  static constexpr int oK = oQ + kTiles * kTileBytes;
-  static constexpr int oV = oK + kStages * kTileBytes;
-  static constexpr int oScale = oV + kStages * kTileBytes;      // [sk | sv][stage][key], cache only
-  static constexpr int oBar = oScale + (KV4 ? 2 * kStages * kKeys * 4 : 0);
-  static constexpr int kNumBars = 2 + 2 + 5 * kStages + 2 + 2 + 2 + 2;
+  static constexpr int oK = oQ + kTiles * kQBytes;
+  static constexpr int oV = oK + kStages * kKVBytes;
+  static constexpr int oScale = oV + kStages * kKVBytes;      // [sk | sv][stage][key], cache only
+  static constexpr int oStage = oScale + (KV4 ? 2 * kStages * kKeys * 4 : 0);  // [softmax warp][row][64 bytes]
+  static constexpr int oBar = oStage + 8 * 32 * 64;
+  static constexpr int kNumBars = 2 + 2 + 5 * kStages + 4 + 4 + 4 + 2;
   static constexpr int oMisc = oBar + kNumBars * 8;
   static constexpr int kSmem = oMisc + 16 + 1024;
   static constexpr int kFirstSoftmax = KV4 ? 8 : 4;
@@ -123,14 +127,28 @@ __device__ __forceinline__ Item get_item(const TileArgs& a, int item, uint32_t* 
   return it;
 }
 
-__device__ __forceinline__ bool wait_t(uint64_t* bar, uint32_t parity, volatile int* abort, uint32_t backoff_ns = 16) {
-  return mbar_wait_ex(bar, parity, abort, backoff_ns) > 0;
+// Waits for a phase with the blocking test (the hardware holds the warp until the
+// phase completes or a short limit passes: three of these sit on the chain S, softmax, P V,
+// where sleeping between polls measured 400 cycles each), at most kWaitLimitNs.
+__device__ __forceinline__ bool wait_t(uint64_t* bar, uint32_t parity, volatile int* abort) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const uint64_t t0 = global_ns();
+  for (uint32_t n = 1;; ++n) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if ((n & 7u) == 0) {
+      if (*abort) return false;
+      if (global_ns() - t0 > kWaitLimitNs) {
+        *abort = 1;
+        return false;
+      }
+    }
+  }
 }
 
 // The same for a whole warp: every lane waits, and all of them go on or none (a
 // wait that gave up must not part the warp before its collectives).
-__device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, volatile int* abort, uint32_t backoff_ns = 16) {
-  const bool got = wait_t(bar, parity, abort, backoff_ns);
+__device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, volatile int* abort) {
+  const bool got = wait_t(bar, parity, abort);
   return __all_sync(0xFFFFFFFFu, got);
 }
 
@@ -151,18 +169,18 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
   uint64_t* const v_full = b; b += C::kStages;     // cross: the copy has landed
   uint64_t* const v_ready = b; b += C::kStages;    // the MMA may read
   uint64_t* const v_empty = b; b += C::kStages;
-  uint64_t* const s_full = b; b += 2;              // [tile]
-  uint64_t* const p_full = b; b += 2;
-  uint64_t* const pv_done = b; b += 2;
+  uint64_t* const s_full = b; b += 4;              // [tile][buffer]
+  uint64_t* const p_full = b; b += 4;
+  uint64_t* const pv_done = b; b += 4;
   uint64_t* const drain = b;
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + C::oMisc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::oMisc + 4);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int i = 0; i < 2; ++i) {
-      mbar_init(q_full + i, 1); mbar_init(q_free + i, 1);
-      mbar_init(s_full + i, 1); mbar_init(p_full + i, 4); mbar_init(pv_done + i, 1); mbar_init(drain + i, 1);
+      mbar_init(q_full + i, 1); mbar_init(q_free + i, 1); mbar_init(drain + i, 1);
     }
+    for (int i = 0; i < 4; ++i) { mbar_init(s_full + i, 1); mbar_init(p_full + i, 4); mbar_init(pv_done + i, 1); }
     for (int i = 0; i < C::kStages; ++i) {
       // cache: four unpacking warps fill a stage; the softmax warps read its scales
       mbar_init(k_full + i, KV4 ? 4 : 1); mbar_init(k_empty + i, KV4 ? 2 + 8 : 2);
@@ -197,10 +215,10 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
         if (it.nb == 0) continue;
         auto load_q = [&]() {
           for (int tt = 0; tt < kTiles && ok; ++tt) {
-            if (!(ok = wait_t(q_free + tt, (li & 1) ^ 1, abort_flag, 64u))) return;
-            mbar_arrive_expect_tx(q_full + tt, C::kTileBytes);
+            if (!(ok = wait_t(q_free + tt, (li & 1) ^ 1, abort_flag))) return;
+            mbar_arrive_expect_tx(q_full + tt, C::kQBytes);
             for (int h = 0; h < C::kHalves; ++h)
-              tma_load_4d(smem + C::oQ + tt * C::kTileBytes + h * C::kHalf, &tm_q, q_full + tt, h * 64,
+              tma_load_4d(smem + C::oQ + tt * C::kQBytes + h * C::kQHalf, &tm_q, q_full + tt, h * 64,
                           it.row0 + tt * kRows, it.h, it.b);
           }
           ++li;
@@ -212,18 +230,18 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
           for (int t = 0; t < it.nb && ok; ++t, ++g) {
             const int s = g % C::kStages, key = it.k0 + t * kKeys;
             const uint32_t par = ((g / C::kStages) & 1) ^ 1;
-            if (!(ok = wait_t(k_empty + s, par, abort_flag, 64u))) break;
-            mbar_arrive_expect_tx(k_full + s, C::kTileBytes);
+            if (!(ok = wait_t(k_empty + s, par, abort_flag))) break;
+            mbar_arrive_expect_tx(k_full + s, C::kKVBytes);
             for (int h = 0; h < C::kHalves; ++h)
-              tma_load_4d(smem + C::oK + s * C::kTileBytes + h * C::kHalf, &tm_k, k_full + s, h * 64, key, hk, it.b);
+              tma_load_4d(smem + C::oK + s * C::kKVBytes + h * C::kHalf, &tm_k, k_full + s, h * 64, key, hk, it.b);
             if (t == 0) {
               load_q();
               if (!ok) break;
             }
-            if (!(ok = wait_t(v_empty + s, par, abort_flag, 64u))) break;
-            mbar_arrive_expect_tx(v_full + s, C::kTileBytes);
+            if (!(ok = wait_t(v_empty + s, par, abort_flag))) break;
+            mbar_arrive_expect_tx(v_full + s, C::kKVBytes);
             for (int h = 0; h < C::kHalves; ++h)
-              tma_load_4d(smem + C::oV + s * C::kTileBytes + h * C::kHalf, &tm_v, v_full + s, h * 64, key, hk, it.b);
+              tma_load_4d(smem + C::oV + s * C::kKVBytes + h * C::kHalf, &tm_v, v_full + s, h * 64, key, hk, it.b);
           }
         }
       }
@@ -239,42 +257,53 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
           while (!mbar_try_wait(q_full + tt, (li - 1) & 1) && ++n < kSpinLimit) {}
     } else if ((warp == 1 || warp == 2) && lane == 0) {
       // ------------------------------------------------------------ MMA issuers
+      // Per tile: P V(g), then S(g + 2) into the buffer whose P it has read (after
+      // it has completed: products into different accumulators are not ordered).
       const int tt = warp - 1;
-      const uint32_t sQ = smem_u32(smem + C::oQ) + tt * C::kTileBytes;
+      const uint32_t sQ = smem_u32(smem + C::oQ) + tt * C::kQBytes;
       const uint32_t sK = smem_u32(smem + C::oK), sV = smem_u32(smem + C::oV);
-      const uint32_t tS = tbase + tt * 128, tO = tbase + 256 + tt * 128;
-      uint32_t g = 0, li = 0;
+      const uint32_t tS0 = tbase + tt * 128, tO = tbase + 256 + tt * 128;
+      uint32_t g0 = 0, li = 0;
+      auto scores = [&](uint32_t g, bool last) -> bool {
+        const int s = g % C::kStages;
+        const uint32_t buf = g & 1;
+        if (!wait_t(k_full + s, (g / C::kStages) & 1, abort_flag)) return false;
+        if (g >= 2 && !wait_t(pv_done + tt * 2 + buf, ((g - 2) >> 1) & 1, abort_flag)) return false;
+        tc_fence_after();
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+          const uint32_t off = (kk & 3) * 32;
+          mma_f16_ss(tS0 + buf * 64, smem_desc(sQ + (kk >> 2) * C::kQHalf + off, 16, 1024, kSwizzle128B),
+                     smem_desc(sK + s * C::kKVBytes + (kk >> 2) * C::kHalf + off, 16, 1024, kSwizzle128B),
+                     C::kIdescQK, kk > 0 ? 1u : 0u);
+        }
+        mma_commit(s_full + tt * 2 + buf);
+        mma_commit(k_empty + s);
+        if (last) mma_commit(q_free + tt);
+        return true;
+      };
       for (int item = blockIdx.x; item < a.nitems && ok; item += gridDim.x) {
         const Item it = get_item<KV4>(a, item, &bad);
         if (it.nb == 0) continue;
-        if (!(ok = wait_t(q_full + tt, li & 1, abort_flag, 32u))) break;
+        if (!(ok = wait_t(q_full + tt, li & 1, abort_flag))) break;
         ++li;
-        for (int t = 0; t < it.nb; ++t, ++g) {
+        for (int t = 0; t < 2 && t < it.nb && ok; ++t) ok = scores(g0 + t, t == it.nb - 1);
+        for (int t = 0; t < it.nb && ok; ++t) {
+          const uint32_t g = g0 + t, buf = g & 1;
           const int s = g % C::kStages;
-          const uint32_t par = (g / C::kStages) & 1;
-          if (!(ok = wait_t(k_full + s, par, abort_flag, 32u))) break;
-          // S takes the columns of the previous block's P.
-          if (g > 0 && !(ok = wait_t(pv_done + tt, (g - 1) & 1, abort_flag, 32u))) break;
-          tc_fence_after();
-#pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk) {
-            const uint32_t off = (kk >> 2) * C::kHalf + (kk & 3) * 32;
-            mma_f16_ss(tS, smem_desc(sQ + off, 16, 1024, kSwizzle128B),
-                       smem_desc(sK + s * C::kTileBytes + off, 16, 1024, kSwizzle128B), C::kIdescQK, kk > 0 ? 1u : 0u);
-          }
-          mma_commit(s_full + tt);
-          mma_commit(k_empty + s);
-          if (t == it.nb - 1) mma_commit(q_free + tt);
-          if (!(ok = wait_t(v_ready + s, par, abort_flag, 32u))) break;
-          if (!(ok = wait_t(p_full + tt, g & 1, abort_flag, 32u))) break;
+          if (!(ok = wait_t(v_ready + s, (g / C::kStages) & 1, abort_flag))) break;
+          if (!(ok = wait_t(p_full + tt * 2 + buf, (g >> 1) & 1, abort_flag))) break;
           tc_fence_after();
 #pragma unroll
           for (int kk = 0; kk < kKeys / 16; ++kk)
-            mma_f16_ts(tO, tS + kk * 8, smem_desc(sV + s * C::kTileBytes + kk * 16 * 128, C::kHalf, 1024, kSwizzle128B),
-                       C::kIdescPV, t > 0 || kk > 0 ? 1u : 0u);
-          mma_commit(pv_done + tt);
+            mma_f16_ts(tO, tS0 + buf * 64 + kk * 8,
+                       smem_desc(sV + s * C::kKVBytes + kk * 16 * 128, C::kHalf, 1024, kSwizzle128B), C::kIdescPV,
+                       t > 0 || kk > 0 ? 1u : 0u);
+          mma_commit(pv_done + tt * 2 + buf);
           mma_commit(v_empty + s);
+          if (t + 2 < it.nb) ok = scores(g + 2, t + 2 == it.nb - 1);
         }
+        g0 += it.nb;
       }
       mma_commit(drain + tt);
       uint32_t n = 0;
@@ -286,13 +315,13 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
         const Item it = get_item<KV4>(a, item, &bad);
         for (int t = 0; t < it.nb; ++t, ++g) {
           const int s = g % C::kStages;
-          if (!(ok = wait_warp(v_full + s, (g / C::kStages) & 1, abort_flag, 64u))) break;
+          if (!(ok = wait_warp(v_full + s, (g / C::kStages) & 1, abort_flag))) break;
           // Rows past Nk are zeros already (filled by the copy).
           const int first = it.len - (it.k0 + t * kKeys), last = min(kKeys, a.Nk - (it.k0 + t * kKeys));
           if (first < last) {
             for (int idx = lane; idx < (last - first) * C::kHalves * 8; idx += 32) {
               const int row = first + idx / (C::kHalves * 8), ch = idx % (C::kHalves * 8);
-              *reinterpret_cast<uint4*>(smem + C::oV + s * C::kTileBytes + (ch >> 3) * C::kHalf + row * 128 +
+              *reinterpret_cast<uint4*>(smem + C::oV + s * C::kKVBytes + (ch >> 3) * C::kHalf + row * 128 +
                                         (ch & 7) * 16) = make_uint4(0, 0, 0, 0);
             }
             fence_proxy_async_smem();
@@ -304,53 +333,47 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
     }
   } else if (KV4 && warp < 8) {
     // -------------------------------------------------------------- unpacking warps
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
     if constexpr (KV4) {
-      constexpr int kQ = D / 32;  // 16-byte pieces of a code row
-      const int row = threadIdx.x - 128;
-      uint4 kr[kQ], vr[kQ];
-      float ks = 0.0f, vs = 0.0f;
-      auto fetch = [&](const Item& it, int t) {
+      constexpr int kQ = D / 64;  // 16-byte pieces of a code row per thread: two threads per key
+      const int row = threadIdx.x & 63, part = (threadIdx.x >> 6) & 1;
+      // Place of this thread's key of block t, or -1 behind the last key.
+      auto place = [&](const Item& it, int t) -> long long {
         const int key = it.k0 + t * kKeys + row;
+        if (t >= it.nb || key >= it.len) return -1;
+        int page = __ldg(a.table + static_cast<size_t>(it.b) * a.max_pages + (key >> a.page_log2));
+        if (page < 0 || page >= a.num_pages) {
+          bad |= kStatusBadPosition;
+          page = 0;
+        }
+        return ((static_cast<long long>(page) * a.heads + it.h) << a.page_log2) + (key & ((1 << a.page_log2) - 1));
+      };
+      auto fetch = [&](const uint8_t* codes, const float* scale, long long at, uint4* w, float& s) {
+        if (at >= 0) {
+          const uint4* const p = reinterpret_cast<const uint4*>(codes + at * (D / 2)) + part * kQ;
 #pragma unroll
-        for (int i = 0; i < kQ; ++i) kr[i] = vr[i] = make_uint4(0, 0, 0, 0);
-        ks = vs = 0.0f;
-        if (key < it.len) {
-          int page = __ldg(a.table + static_cast<size_t>(it.b) * a.max_pages + (key >> a.page_log2));
-          if (page < 0 || page >= a.num_pages) {
-            bad |= kStatusBadPosition;
-            page = 0;
-          }
-          const size_t at = ((static_cast<size_t>(page) * a.heads + it.h) << a.page_log2) + (key & ((1 << a.page_log2) - 1));
-          const uint4* kp = reinterpret_cast<const uint4*>(a.k4 + at * (D / 2));
-          const uint4* vp = reinterpret_cast<const uint4*>(a.v4 + at * (D / 2));
+          for (int i = 0; i < kQ; ++i) w[i] = __ldg(p + i);
+          s = __ldg(scale + at);
+        } else {
 #pragma unroll
-          for (int i = 0; i < kQ; ++i) {
-            kr[i] = __ldg(kp + i);
-            vr[i] = __ldg(vp + i);
-          }
-          ks = __ldg(a.sk + at);
-          vs = __ldg(a.sv + at);
+          for (int i = 0; i < kQ; ++i) w[i] = make_uint4(0, 0, 0, 0);
+          s = 0.0f;
         }
       };
       uint32_t g = 0;
       for (int item = blockIdx.x; item < a.nitems && ok; item += gridDim.x) {
         const Item it = get_item<KV4>(a, item, &bad);
-        if (it.nb > 0) fetch(it, 0);
+        long long at = place(it, 0);
+        uint4 k[kQ], v[kQ];
+        float ks, vs;
+        fetch(a.k4, a.sk, at, k, ks);
         for (int t = 0; t < it.nb; ++t, ++g) {
-          uint4 k[kQ], v[kQ];
-#pragma unroll
-          for (int i = 0; i < kQ; ++i) {
-            k[i] = kr[i];
-            v[i] = vr[i];
-          }
-          const float ks_now = ks, vs_now = vs;
-          if (t + 1 < it.nb) fetch(it, t + 1);
           const int s = g % C::kStages;
           const uint32_t par = ((g / C::kStages) & 1) ^ 1;
-          if (!(ok = wait_warp(k_empty + s, par, abort_flag, 64u))) break;
-          uint8_t* const kt = smem + C::oK + s * C::kTileBytes + row * 128;
-          uint8_t* const vt = smem + C::oV + s * C::kTileBytes + row * 128;
+          fetch(a.v4, a.sv, at, v, vs);
+          if (!(ok = wait_warp(k_empty + s, par, abort_flag))) break;
+          uint8_t* const kt = smem + C::oK + s * C::kKVBytes + row * 128;
+          uint8_t* const vt = smem + C::oV + s * C::kKVBytes + row * 128;
 #pragma unroll
           for (int i = 0; i < kQ; ++i) {
             const uint32_t w[4] = {k[i].x, k[i].y, k[i].z, k[i].w};
@@ -360,15 +383,17 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
               const uint32_t p2 = codes_bf16(w[c] >> 8), p3 = codes_bf16(w[c] >> 12);
               const uint4 o = make_uint4(__byte_perm(p0, p1, 0x5410), __byte_perm(p2, p3, 0x5410),
                                          __byte_perm(p0, p1, 0x7632), __byte_perm(p2, p3, 0x7632));
-              const int ch = i * 4 + c;
+              const int ch = (part * kQ + i) * 4 + c;
               *reinterpret_cast<uint4*>(kt + (ch >> 3) * C::kHalf + (((ch & 7) ^ (row & 7)) << 4)) = o;
             }
           }
-          scales[s * kKeys + row] = ks_now * a.scale_log2;
+          if (part == 0) scales[s * kKeys + row] = ks * a.scale_log2;
           fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) mbar_arrive(k_full + s);
-          if (!(ok = wait_warp(v_empty + s, par, abort_flag, 64u))) break;
+          at = place(it, t + 1);  // the next block's codes travel under this block's values
+          fetch(a.k4, a.sk, at, k, ks);
+          if (!(ok = wait_warp(v_empty + s, par, abort_flag))) break;
 #pragma unroll
           for (int i = 0; i < kQ; ++i) {
             const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
@@ -376,11 +401,11 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
             for (int c = 0; c < 4; ++c) {  // channels 0 4 1 5 2 6 3 7 of eight; the epilogue puts them right
               const uint4 o = make_uint4(codes_bf16(w[c]), codes_bf16(w[c] >> 4), codes_bf16(w[c] >> 8),
                                          codes_bf16(w[c] >> 12));
-              const int ch = i * 4 + c;
+              const int ch = (part * kQ + i) * 4 + c;
               *reinterpret_cast<uint4*>(vt + (ch >> 3) * C::kHalf + (((ch & 7) ^ (row & 7)) << 4)) = o;
             }
           }
-          scales[(C::kStages + s) * kKeys + row] = vs_now;
+          if (part == 0) scales[(C::kStages + s) * kKeys + row] = vs;
           fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) mbar_arrive(v_ready + s);
@@ -389,12 +414,12 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
     }
   } else {
     // -------------------------------------------------------------- softmax, one row per thread
-    if constexpr (KV4) asm volatile("setmaxnreg.inc.sync.aligned.u32 176;");
+    if constexpr (KV4) asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
     else asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
     const int tt = (warp - C::kFirstSoftmax) >> 2;
     const int quad = warp & 3;
     const uint32_t lane_off = static_cast<uint32_t>(quad * 32) << 16;
-    const uint32_t tS = tbase + tt * 128 + lane_off, tO = tbase + 256 + tt * 128 + lane_off;
+    const uint32_t tS0 = tbase + tt * 128 + lane_off, tO = tbase + 256 + tt * 128 + lane_off;
     uint32_t g = 0;
     for (int item = blockIdx.x; item < a.nitems && ok; item += gridDim.x) {
       const Item it = get_item<KV4>(a, item, &bad);
@@ -408,7 +433,8 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
       }
       float m = -INFINITY, l = 0.0f;
       for (int t = 0; t < it.nb; ++t, ++g) {
-        if (!(ok = wait_warp(s_full + tt, g & 1, abort_flag))) break;
+        const uint32_t buf = g & 1, tS = tS0 + buf * 64;
+        if (!(ok = wait_warp(s_full + tt * 2 + buf, (g >> 1) & 1, abort_flag))) break;
         tc_fence_after();
         uint32_t raw[kKeys];
         tmem_ld_row<kKeys>(tS, raw);
@@ -450,7 +476,9 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
           m = mb;
           l *= f;
         }
-        if (any_up && t > 0) {
+        if (any_up && t > 0) {  // O holds the blocks before this one
+          if (!(ok = wait_warp(pv_done + tt * 2 + (buf ^ 1), ((g - 1) >> 1) & 1, abort_flag))) break;
+          tc_fence_after();
           const float2 f2 = make_float2(f, f);
 #pragma unroll
           for (int c = 0; c < D; c += 32) {
@@ -504,13 +532,13 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
         tc_fence_before();
         __syncwarp();
         if (lane == 0) {
-          mbar_arrive(p_full + tt);
+          mbar_arrive(p_full + tt * 2 + buf);
           if constexpr (KV4) mbar_arrive(v_empty + stg);
         }
       }
       if (!ok) break;
       if (it.nb > 0) {
-        if (!(ok = wait_warp(pv_done + tt, (g - 1) & 1, abort_flag))) break;
+        if (!(ok = wait_warp(pv_done + tt * 2 + ((g - 1) & 1), ((g - 1) >> 1) & 1, abort_flag))) break;
         tc_fence_after();
       }
       const bool some = m != -INFINITY;
@@ -520,7 +548,26 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
       const size_t at = bh * a.R + r;
       const bool split = KV4 && a.nsplit > 1;
       const size_t prow = static_cast<size_t>(it.split) * (a.nitems / (a.npairs * a.nsplit)) * a.R + at;
-      __nv_bfloat16* const orow = a.out + it.b * a.os.b + it.h * a.os.h + r * a.os.n;
+      // Rows leave through shared memory, 64 bytes of each at a time: four lanes
+      // write a row's piece together (a thread writing its own row touched 32
+      // lines per store, 1900 cycles a block at 4 blocks per item).
+      const uint32_t live = __ballot_sync(0xFFFFFFFFu, row_live);
+      uint8_t* const stage = smem + C::oStage + (warp - C::kFirstSoftmax) * (32 * 64);
+      const int rbase = it.row0 + tt * kRows + quad * 32;
+      auto put = [&](const uint32_t* w, uint8_t* base, int64_t row_bytes) {  // 16 words of each row
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          *reinterpret_cast<uint4*>(stage + lane * 64 + ((i ^ ((lane >> 1) & 3)) << 4)) =
+              make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int row = 8 * i + (lane >> 2), ch = lane & 3;
+          const uint4 v = *reinterpret_cast<const uint4*>(stage + row * 64 + ((ch ^ ((row >> 1) & 3)) << 4));
+          if ((live >> row) & 1u) *reinterpret_cast<uint4*>(base + row * row_bytes + ch * 16) = v;
+        }
+        __syncwarp();
+      };
 #pragma unroll
       for (int c = 0; c < D; c += 32) {
         uint32_t o[32];
@@ -535,21 +582,18 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
         for (int i = 0; i < 32; ++i) {
           // cache: column 2i + e of eight holds channel i + 4e
           const int from = KV4 ? (i & ~7) + 2 * (i & 3) + ((i >> 2) & 1) : i;
-          x[i] = __uint_as_float(o[from]) * inv;
-          if (!some) x[i] = 0.0f;
+          x[i] = some ? __uint_as_float(o[from]) * inv : 0.0f;
         }
-        if (row_live && split) {
-          float4* const dst = reinterpret_cast<float4*>(a.parts.o + prow * D + c);
+        if (split) {
+          uint8_t* const dst = reinterpret_cast<uint8_t*>(a.parts.o + (prow - lane) * D + c);
+          put(reinterpret_cast<const uint32_t*>(x), dst, D * 4);
+          put(reinterpret_cast<const uint32_t*>(x + 16), dst + 64, D * 4);
+        } else {
+          uint32_t w[16];
 #pragma unroll
-          for (int i = 0; i < 32; i += 4) dst[i / 4] = make_float4(x[i], x[i + 1], x[i + 2], x[i + 3]);
-        } else if (row_live) {
-#pragma unroll
-          for (int i = 0; i < 32; i += 8)
-            *reinterpret_cast<uint4*>(orow + c + i) =
-                make_uint4(pack_bf16(x[i], x[i + 1]), pack_bf16(x[i + 2], x[i + 3]), pack_bf16(x[i + 4], x[i + 5]),
-                           pack_bf16(x[i + 6], x[i + 7]));
+          for (int i = 0; i < 16; ++i) w[i] = pack_bf16(x[2 * i], x[2 * i + 1]);
+          put(w, reinterpret_cast<uint8_t*>(a.out + it.b * a.os.b + it.h * a.os.h + rbase * a.os.n + c), a.os.n * 2);
         }
-        __syncwarp();
       }
       tc_fence_before();
       if (row_live) {
@@ -579,9 +623,9 @@ PFN_cuTensorMapEncodeTiled_v12000 get_encoder_t() {
   return fn;
 }
 
-// 4D map over bf16 [B, H, N, D] with strides; box = 64 channels x 128 rows,
+// 4D map over bf16 [B, H, N, D] with strides; box = 64 channels x `rows`,
 // 128-byte swizzle, zeros past N.
-bool make_map(CUtensorMap* m, const void* base, int B, int H, int N, int D, const ra_strides& st) {
+bool make_map(CUtensorMap* m, const void* base, int B, int H, int N, int D, const ra_strides& st, int rows) {
   auto enc = get_encoder_t();
   if (!enc) return false;
   // The stride of an extent of one is free; the map wants a valid one.
@@ -591,7 +635,7 @@ bool make_map(CUtensorMap* m, const void* base, int B, int H, int N, int D, cons
                         static_cast<cuuint64_t>(B)};
   cuuint64_t strides[3] = {static_cast<cuuint64_t>(sn) * 2, static_cast<cuuint64_t>(sh) * 2,
                            static_cast<cuuint64_t>(sb) * 2};
-  cuuint32_t box[4] = {64, static_cast<cuuint32_t>(kRows), 1, 1};
+  cuuint32_t box[4] = {64, static_cast<cuuint32_t>(rows), 1, 1};
   cuuint32_t es[4] = {1, 1, 1, 1};
   return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides, box, es,
              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
@@ -631,7 +675,7 @@ cudaError_t launch_kv4_tiles(const ra_kv4_cache& c, const ra_kv4_attn& at, const
   a.max_pages = at.max_pages; a.Nq = at.Nq; a.causal = at.causal;
   a.parts = parts;
   CUtensorMap mq;
-  if (!make_map(&mq, q, at.B, c.Hk, a.R, c.D, a.os)) return cudaErrorInvalidValue;
+  if (!make_map(&mq, q, at.B, c.Hk, a.R, c.D, a.os, kRows)) return cudaErrorInvalidValue;
   return c.D == 64 ? launch_tiles<64, true>(mq, mq, mq, a, st) : launch_tiles<128, true>(mq, mq, mq, a, st);
 }
 
@@ -650,8 +694,8 @@ cudaError_t launch_attn_cross(const ra_cross_problem& p, const void* q, const ra
   a.kv_lens = kv_lens;
   a.Nk = p.Nk;
   CUtensorMap mq, mk, mv;
-  if (!make_map(&mq, q, p.B, p.H, p.Nq, p.D, qs) || !make_map(&mk, k, p.B, p.Hk, p.Nk, p.D, ks) ||
-      !make_map(&mv, v, p.B, p.Hk, p.Nk, p.D, vs))
+  if (!make_map(&mq, q, p.B, p.H, p.Nq, p.D, qs, kRows) || !make_map(&mk, k, p.B, p.Hk, p.Nk, p.D, ks, kKeys) ||
+      !make_map(&mv, v, p.B, p.Hk, p.Nk, p.D, vs, kKeys))
     return cudaErrorInvalidValue;
   return p.D == 64 ? launch_tiles<64, false>(mq, mk, mv, a, st) : launch_tiles<128, false>(mq, mk, mv, a, st);
 }
