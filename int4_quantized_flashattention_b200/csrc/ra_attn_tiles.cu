@@ -7,7 +7,18 @@
 // per tile, so the tensor cores work on one block while the softmax is at the
 // other: with 128-key blocks and one buffer a tile's products and its softmax
 // took turns (890 TFLOP/s at 8192 x 8192, D = 128, softmax warps idle half of
-// the time).
+// the time; 1157 now).  The two tiles' warps of a quarter share an SM partition and
+// its exponentials (8 cycles a warp instruction, 512 a block); left alone they
+// fell into step, both at the exponentials or both at none.  They take turns
+// (turn_of): 732 cycles a block for a warp's exponentials instead of 1150.
+// What bounds it, at D = 128: shared memory, 1280 of 1750 cycles a block (S with
+// N = 64 reads Q again for every block, 48 cycles an MMA against 32 of
+// arithmetic; P V 64), and the hops between the MMAs and the softmax; at D = 64
+// the exponentials.  Measured and left out: exponentials of every 4th to 12th
+// pair by a polynomial (2 to 12 % slower), P beside S so that S(g + 1) need not
+// wait for P V(g - 1) (4 % slower), 16 softmax warps (6 % slower, 20 % for the
+// cache), four warps of their own for the output (6 % slower at 8192 keys, 3 %
+// faster at 512, 13 % slower at 128).
 //   warp 0      TMA producer: Q, and (cross) K and V, 64-channel boxes with the
 //               128-byte swizzle
 //   warps 1, 2  MMA issuers of tiles 0 and 1: S = Q K^T into TMEM (tcgen05
@@ -57,7 +68,7 @@ struct CfgT {
   static constexpr int oScale = oV + kStages * kKVBytes;      // [sk | sv][stage][key], cache only
   static constexpr int oStage = oScale + (KV4 ? 2 * kStages * kKeys * 4 : 0);  // [softmax warp][row][64 bytes]
   static constexpr int oBar = oStage + 8 * 32 * 64;
-  static constexpr int kNumBars = 2 + 2 + 5 * kStages + 4 + 4 + 4 + 2;
+  static constexpr int kNumBars = 2 + 2 + 5 * kStages + 4 + 4 + 4 + 2 + 8;
   static constexpr int oMisc = oBar + kNumBars * 8;
   static constexpr int kSmem = oMisc + 16 + 1024;
   static constexpr int kFirstSoftmax = KV4 ? 8 : 4;
@@ -172,6 +183,7 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
   uint64_t* const s_full = b; b += 4;              // [tile][buffer]
   uint64_t* const p_full = b; b += 4;
   uint64_t* const pv_done = b; b += 4;
+  uint64_t* const turn_of = b; b += 8;             // [tile][quarter]: whose exponentials run
   uint64_t* const drain = b;
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + C::oMisc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::oMisc + 4);
@@ -186,6 +198,7 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
       mbar_init(k_full + i, KV4 ? 4 : 1); mbar_init(k_empty + i, KV4 ? 2 + 8 : 2);
       mbar_init(v_full + i, 1); mbar_init(v_ready + i, KV4 ? 4 : 1); mbar_init(v_empty + i, KV4 ? 2 + 8 : 2);
     }
+    for (int i = 0; i < 8; ++i) mbar_init(turn_of + i, 1);
     *abort_flag = 0;
     fence_barrier_init();
   }
@@ -496,6 +509,7 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
         const float mr = m == -INFINITY ? 0.0f : m;
         const float2 c2 = make_float2(a.scale_log2, a.scale_log2), m2 = make_float2(-mr, -mr);
         float2 sum2 = make_float2(0.0f, 0.0f);
+        if (!(ok = wait_warp(turn_of + tt * 4 + quad, (g & 1) ^ (tt ^ 1), abort_flag))) break;
 #pragma unroll
         for (int c = 0; c < kKeys; c += 32) {
           uint32_t w[16];
@@ -527,6 +541,7 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
           tmem_st_row_nw<16>(tS + c / 2, w);
         }
         if (!ok) break;
+        if (lane == 0) mbar_arrive(turn_of + (tt ^ 1) * 4 + quad);
         l += sum2.x + sum2.y;
         tmem_wait_st();
         tc_fence_before();
