@@ -147,11 +147,14 @@ __global__ void __launch_bounds__(kThreads) kv4_read_kernel(const CacheArgs a) {
 //     costs half of what rows as M would.  tcgen05 (M >= 64) would spend 128
 //     rows on one.  The channels of a k step are free to choose as long as Q
 //     uses the same: a lane's 16 bytes of a key are its four words, and the
-//     nibbles j and j + 4 of a word make a bf16 pair without moving bits:
-//     (w >> 4j) & 0x000F000F, XOR 0x43084308, is the pair 128 + 8 + code,
-//     exact in bf16, and one subtraction gives the codes.
-//   * The keys' scales multiply S in fp32 and P before its one rounding to
-//     bf16, so the products see the exact codes.
+//     nibbles j and j + 4 of a word make an f16 pair (codes_f16_lo / _hi).
+//   * Products run in f16, in which the codes are exact.  Q's rows are brought to
+//     a largest value of about 2^14 by a power of two: f16's 11 bits hold bf16's
+//     8, and what lies 2^28 below a row's largest value loses bits.  The keys'
+//     scales multiply S in fp32.  The values' scales multiply P in fp32, relative
+//     to a power of two not below the largest so far (vref), so that the one
+//     rounding of P to f16 costs 2^-11 (bf16 cost 2^-8: 1.6 times the error of the
+//     output's own rounding; now none that shows).
 //   * O^T = V^T P^T, again 16 channels by 8 rows: P^T comes out of S^T by one
 //     8x8 transpose per 8 keys, V^T by pairing the words of two keys.  The
 //     pairs are keys x and x + 4 of each eight, which puts the rows that the
@@ -175,7 +178,8 @@ struct RowsArgs {
 constexpr int kRowWarps = 4;
 constexpr int kStep = 32;    // keys per warp and step
 constexpr int kStages = 3;
-constexpr float kLazy = 8.0f;  // the reference maximum moves when a score passes it by this (powers of two)
+constexpr float kLazy = 4.0f;  // the reference maximum moves when a score passes it by this (powers of two)
+constexpr float kPUp = 2048.0f;  // P goes to f16 times this: at most 2^(4 + 11), below 2^-25 it loses bits
 
 template <int D>
 struct RowsCfg {
@@ -250,21 +254,44 @@ __global__ void __launch_bounds__(kRowWarps * 32) kv4_rows_kernel(const RowsArgs
 
   // Q fragments: row 8j + g, the channels of this lane's words.
   uint32_t qf[NT][2 * kW][2];
+  float qscale[NT][2];  // of rows 8j + 2 q4 + {0, 1}: what the scores are multiplied with
   int lim[NT][2];
   int lim_min = len;
 #pragma unroll
   for (int j = 0; j < NT; ++j) {
     const int r = r0 + 8 * j + g;
-    const bool ok = r < R && r % a.Nq < ql;
-    const __nv_bfloat16* const src = a.q + (static_cast<size_t>(bh) * R + (ok ? r : 0)) * D + q4 * (D / 4);
+    const bool in_use = r < R && r % a.Nq < ql;
+    const __nv_bfloat16* const src = a.q + (static_cast<size_t>(bh) * R + (in_use ? r : 0)) * D + q4 * (D / 4);
+    uint4 u[kW];
+    float most = 0.0f;
 #pragma unroll
     for (int w = 0; w < kW; ++w) {
-      const uint4 u = ok ? __ldg(reinterpret_cast<const uint4*>(src + 8 * w)) : make_uint4(0, 0, 0, 0);
-      qf[j][2 * w][0] = __byte_perm(u.x, u.z, 0x5410);      // channels 0, 4
-      qf[j][2 * w][1] = __byte_perm(u.x, u.z, 0x7632);      // 1, 5
-      qf[j][2 * w + 1][0] = __byte_perm(u.y, u.w, 0x5410);  // 2, 6
-      qf[j][2 * w + 1][1] = __byte_perm(u.y, u.w, 0x7632);  // 3, 7
+      u[w] = in_use ? __ldg(reinterpret_cast<const uint4*>(src + 8 * w)) : make_uint4(0, 0, 0, 0);
+      const uint32_t x[4] = {u[w].x, u[w].y, u[w].z, u[w].w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        most = fmaxf(most, fmaxf(fabsf(__uint_as_float(x[i] << 16)), fabsf(__uint_as_float(x[i] & 0xFFFF0000u))));
     }
+    most = fmaxf(most, __shfl_xor_sync(0xFFFFFFFFu, most, 1));
+    most = fmaxf(most, __shfl_xor_sync(0xFFFFFFFFu, most, 2));
+    // 2^(14 - exponent of the row's largest value), within what has a normal inverse
+    const int ex = max(static_cast<int>(__float_as_uint(most) >> 23), 15);
+    const float up = __uint_as_float(static_cast<uint32_t>(min(127 + 14 - (ex - 127), 253)) << 23);
+    auto pair = [&](uint32_t lo, uint32_t hi, bool odd) {  // channels c and c + 4
+      const float x = __uint_as_float(odd ? lo & 0xFFFF0000u : lo << 16);
+      const float y = __uint_as_float(odd ? hi & 0xFFFF0000u : hi << 16);
+      return pack_f16(x * up, y * up);
+    };
+#pragma unroll
+    for (int w = 0; w < kW; ++w) {
+      qf[j][2 * w][0] = pair(u[w].x, u[w].z, false);      // channels 0, 4
+      qf[j][2 * w][1] = pair(u[w].x, u[w].z, true);       // 1, 5
+      qf[j][2 * w + 1][0] = pair(u[w].y, u[w].w, false);  // 2, 6
+      qf[j][2 * w + 1][1] = pair(u[w].y, u[w].w, true);   // 3, 7
+    }
+    const float down = a.scale_log2 / up;
+#pragma unroll
+    for (int e = 0; e < 2; ++e) qscale[j][e] = __shfl_sync(0xFFFFFFFFu, down, (2 * q4 + e) * 4);
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
       const int rr = r0 + 8 * j + 2 * q4 + e, i = rr % a.Nq;
@@ -275,6 +302,7 @@ __global__ void __launch_bounds__(kRowWarps * 32) kv4_rows_kernel(const RowsArgs
 
   float acc[NT][kM][4];
   float m[NT][2], l[NT][2];
+  float vref = 9.8607613e-32f;  // 2^-103
 #pragma unroll
   for (int j = 0; j < NT; ++j) {
 #pragma unroll
@@ -309,12 +337,12 @@ __global__ void __launch_bounds__(kRowWarps * 32) kv4_rows_kernel(const RowsArgs
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
           uint32_t af[4];
-          af[0] = codes_bf16(w0[w] >> (8 * k));
-          af[1] = codes_bf16(w1[w] >> (8 * k));
-          af[2] = codes_bf16(w0[w] >> (8 * k + 4));
-          af[3] = codes_bf16(w1[w] >> (8 * k + 4));
+          af[0] = codes_f16_lo(w0[w] >> (8 * k));
+          af[1] = codes_f16_lo(w1[w] >> (8 * k));
+          af[2] = codes_f16_hi(w0[w] >> (8 * k));
+          af[3] = codes_f16_hi(w1[w] >> (8 * k));
 #pragma unroll
-          for (int j = 0; j < NT; ++j) mma_bf16(s[j][u], af, qf[j][2 * w + k][0], qf[j][2 * w + k][1]);
+          for (int j = 0; j < NT; ++j) mma_f16(s[j][u], af, qf[j][2 * w + k][0], qf[j][2 * w + k][1]);
         }
     }
     // ---- scores in powers of two, masked; the reference maximum
@@ -323,23 +351,32 @@ __global__ void __launch_bounds__(kRowWarps * 32) kv4_rows_kernel(const RowsArgs
     const int kbase = t * kStep + key_of(g);
     const bool edge = t * kStep + kStep > lim_min;
     bool up = false;
+    float fv[2][2];  // the values' scales; slots behind the last key may hold anything: 0 * NaN is not 0
 #pragma unroll
     for (int u = 0; u < 2; ++u)
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        const float f = skp[16 * u + 8 * e] * a.scale_log2;
+        fv[u][e] = kbase + 16 * u + 8 * e < len ? svp[16 * u + 8 * e] : 0.0f;
+        up |= fv[u][e] > vref;
+        const float f = skp[16 * u + 8 * e];
         const int key = kbase + 16 * u + 8 * e;
 #pragma unroll
         for (int j = 0; j < NT; ++j)
 #pragma unroll
           for (int n = 0; n < 2; ++n) {
             float& y = s[j][u][2 * e + n];
-            y *= f;
+            y *= f * qscale[j][n];
             if (edge && key >= lim[j][n]) y = -INFINITY;
             up |= y > m[j][n] + kLazy;
           }
       }
     if (__any_sync(0xFFFFFFFFu, up)) {
+      float v = fmaxf(fmaxf(fv[0][0], fv[0][1]), fmaxf(fv[1][0], fv[1][1]));
+#pragma unroll
+      for (int o = 4; o < 32; o <<= 1) v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, o));
+      v = fmaxf(vref, __uint_as_float((__float_as_uint(v) + 0x007FFFFFu) & 0x7F800000u));  // a power of two
+      const float fr = vref / v;
+      vref = v;
 #pragma unroll
       for (int j = 0; j < NT; ++j) {
         float f[2];
@@ -352,6 +389,7 @@ __global__ void __launch_bounds__(kRowWarps * 32) kv4_rows_kernel(const RowsArgs
           f[n] = mn == -INFINITY ? 1.0f : ex2_approx(m[j][n] - mn);
           m[j][n] = mn;
           l[j][n] *= f[n];
+          f[n] *= fr;
         }
 #pragma unroll
         for (int i = 0; i < kM; ++i) {
@@ -363,13 +401,13 @@ __global__ void __launch_bounds__(kRowWarps * 32) kv4_rows_kernel(const RowsArgs
       }
     }
     // ---- P^T (times the values' scales) and O^T
+    const float vinv = kPUp / vref;
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
       uint32_t pb[NT][2];
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        // Slots behind the last key may hold anything: 0 * NaN is not 0.
-        const float fv = kbase + 16 * u + 8 * e < len ? svp[16 * u + 8 * e] : 0.0f;
+        const float fr = fv[u][e] * vinv;
 #pragma unroll
         for (int j = 0; j < NT; ++j) {
           float p[2];
@@ -379,7 +417,7 @@ __global__ void __launch_bounds__(kRowWarps * 32) kv4_rows_kernel(const RowsArgs
             p[n] = ex2_approx(s[j][u][2 * e + n] - mr);
             l[j][n] += p[n];
           }
-          pb[j][e] = transpose8(pack_bf16(p[0] * fv, p[1] * fv));
+          pb[j][e] = transpose8(pack_f16(p[0] * fr, p[1] * fr));
         }
       }
       constexpr int kVW = D / 64;  // code words of a key per lane (V)
@@ -398,12 +436,13 @@ __global__ void __launch_bounds__(kRowWarps * 32) kv4_rows_kernel(const RowsArgs
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const int nib = i + (e & 1) * kM;              // 0 .. D/8 - 1
-          const int w = nib >> 3, half = (nib >> 2) & 1, sh = 4 * (nib & 3);
+          const int w = nib >> 3, half = (nib >> 2) & 1, sh = 8 * ((nib >> 1) & 1);
           const uint32_t x0 = x[(e >> 1) * 2][w], x1 = x[(e >> 1) * 2 + 1][w];
-          af[e] = codes_bf16(__byte_perm(x0, x1, half ? 0x7632 : 0x5410) >> sh);
+          const uint32_t pw = __byte_perm(x0, x1, half ? 0x7632 : 0x5410) >> sh;
+          af[e] = (nib & 1) ? codes_f16_hi(pw) : codes_f16_lo(pw);
         }
 #pragma unroll
-        for (int j = 0; j < NT; ++j) mma_bf16(acc[j][i], af, pb[j][0], pb[j][1]);
+        for (int j = 0; j < NT; ++j) mma_f16(acc[j][i], af, pb[j][0], pb[j][1]);
       }
     }
   }
@@ -429,7 +468,7 @@ __global__ void __launch_bounds__(kRowWarps * 32) kv4_rows_kernel(const RowsArgs
     for (int i = 0; i < kM; ++i)
 #pragma unroll
       for (int e = 0; e < 4; ++e)
-        ro[(warp * kRows + 8 * j + 2 * q4 + (e & 1)) * D + g * (D / 8) + i + (e >> 1) * kM] = acc[j][i][e];
+        ro[(warp * kRows + 8 * j + 2 * q4 + (e & 1)) * D + g * (D / 8) + i + (e >> 1) * kM] = acc[j][i][e] * (vref / kPUp);
     if (g == 0) {
 #pragma unroll
       for (int n = 0; n < 2; ++n) {

@@ -3,6 +3,7 @@
 #pragma once
 
 #include <cuda_bf16.h>
+#include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
 #include <cstdint>
@@ -31,6 +32,30 @@ __device__ __forceinline__ uint32_t codes_bf16(uint32_t w) {
   return *reinterpret_cast<const uint32_t*>(&r);
 }
 
+// The same as f16 pairs, from bits 0-3 and 16-19, and from bits 4-7 and 20-23: f16
+// has ten mantissa bits, so the second pair needs no shift (1024 + 16 (code + 8),
+// times 1/16 and minus 72 in one exact fused operation).  Shifts and masks are what
+// bounds the kernels that unpack in registers: a word takes five of them, in bf16
+// seven.
+__device__ __forceinline__ uint32_t codes_f16_lo(uint32_t w) {
+  const uint32_t x = (w & 0x000F000Fu) ^ 0x64086408u;
+  const uint32_t k1032 = 0x64086408u;
+  const __half2 r = __hsub2(*reinterpret_cast<const __half2*>(&x), *reinterpret_cast<const __half2*>(&k1032));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+__device__ __forceinline__ uint32_t codes_f16_hi(uint32_t w) {
+  const uint32_t x = (w & 0x00F000F0u) ^ 0x64806480u;
+  const uint32_t k16th = 0x2C002C00u, k72 = 0xD480D480u;  // 1/16 and -72, twice
+  const __half2 r = __hfma2(*reinterpret_cast<const __half2*>(&x), *reinterpret_cast<const __half2*>(&k16th),
+                            *reinterpret_cast<const __half2*>(&k72));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&h);
@@ -50,10 +75,10 @@ __device__ __forceinline__ void load_words(const uint8_t* p, uint32_t* w) {
   }
 }
 
-// c += a b, bf16 in, fp32 out: a 16 x 16 (row), b 16 x 8 (column).
-__device__ __forceinline__ void mma_bf16(float* c, const uint32_t* a, uint32_t b0, uint32_t b1) {
+// c += a b, f16 in, fp32 out: a 16 x 16 (row), b 16 x 8 (column).
+__device__ __forceinline__ void mma_f16(float* c, const uint32_t* a, uint32_t b0, uint32_t b1) {
   asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }

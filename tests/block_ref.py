@@ -88,7 +88,10 @@ def attention(q, k, v, ends, scale):
     error bounds of both:
       * S has D products and the key's scale in fp32: |dS| <= delta = (D + 8) u32 scale sum_d |q_d k_d| (its largest);
       * P = exp(S - m): relative error delta, plus 2^-18 for the exponential, the lazily moved reference and sums;
-      * P times the value's scale is rounded to bf16 once, the output once more."""
+      * P times the value's scale is rounded to bf16 once, the output once more.  (The few-row kernel over the cache
+        rounds to f16 instead, to 2^-11 and never worse than 2^-25 of 2^-11 times a power of two that is at most twice
+        the largest value scale: an absolute part of 2^-36 * 2 * s_max * |code| <= 2^-35 max|v| per key, divided by
+        the row's sum, which is at least 1 because a key has the reference maximum itself.)"""
     H, n, D = q.shape
     g = H // k.shape[0]
     out = torch.zeros(H, n, D, dtype=torch.float64, device=q.device)
@@ -109,7 +112,8 @@ def attention(q, k, v, ends, scale):
         p = torch.softmax(s, 1)
         o = p @ live_v
         out[h, some], lse[h, some] = o, torch.logsumexp(s, 1)
-        bound[h, some] = UB16 * o.abs() + (UB16 + 2 * delta + 2.0 ** -18) * (1 + UB16) * (p @ live_v.abs())
+        bound[h, some] = (UB16 * o.abs() + (UB16 + 2 * delta + 2.0 ** -18) * (1 + UB16) * (p @ live_v.abs())
+                          + 2.0 ** -35 * m * live_v.abs().max())
         bound_lse[h, some] = (delta[:, 0] + 2.0 ** -18 + 4 * U32 * lse[h, some].abs())
     return out, lse, bound, bound_lse
 
