@@ -148,9 +148,9 @@ __global__ void __launch_bounds__(kThreads) kv4_read_kernel(const CacheArgs a) {
 //     rows on one.  The channels of a k step are free to choose as long as Q
 //     uses the same: a lane's 16 bytes of a key are its four words, and the
 //     nibbles j and j + 4 of a word make an f16 pair (codes_f16_lo / _hi).
-//   * Products run in f16, in which the codes are exact.  Q's rows are brought to
-//     a largest value of about 2^14 by a power of two: f16's 11 bits hold bf16's
-//     8, and what lies 2^28 below a row's largest value loses bits.  The keys'
+//   * Products run in f16, in which the codes are exact.  Q's rows of the CTA are
+//     brought to a largest value of about 2^14 by a power of two: f16's 11 bits
+//     hold bf16's 8, and what lies 2^28 below the largest value loses bits.  The keys'
 //     scales multiply S in fp32.  The values' scales multiply P in fp32, relative
 //     to a power of two not below the largest so far (vref), so that the one
 //     rounding of P to f16 costs 2^-11 (bf16 cost 2^-8: 1.6 times the error of the
@@ -179,6 +179,7 @@ constexpr int kRowWarps = 4;
 constexpr int kStep = 32;    // keys per warp and step
 constexpr int kStages = 3;
 constexpr float kLazy = 4.0f;  // the reference maximum moves when a score passes it by this (powers of two)
+constexpr float kNone = -1e30f;  // reference of a row that has met no key: finite, so that -inf - kNone is -inf
 constexpr float kPUp = 2048.0f;  // P goes to f16 times this: at most 2^(4 + 11), below 2^-25 it loses bits
 
 template <int D>
@@ -217,35 +218,42 @@ __global__ void __launch_bounds__(kRowWarps * 32) kv4_rows_kernel(const RowsArgs
   const int per = (nstep + a.nsplit - 1) / a.nsplit;
   const int t0 = min(split * per, nstep), t1 = min(t0 + per, nstep);
 
-  uint8_t* const ring = smem + warp * kStages * C::kStage;
+  // A step's copies: lane x copies the 16 bytes at 16 x of every 512 (of K and of
+  // V), lanes 0-7 the scales.  Everything that does not change is computed here.
+  constexpr int kCopies = 16 * C::kRow / 512;  // per 16 keys, and 8 keys apart where there are two
+  const int x0 = lane / C::kChunks, ch0 = lane % C::kChunks;
+  const uint32_t ring = smem_u32(smem) + warp * kStages * C::kStage;
+  const uint32_t kdst = k_place(x0) * C::kRow + ch0 * 16;
+  const uint32_t vdst = C::oV + x0 * C::kRow + (C::kChunks == 4 ? ch0 ^ (x0 & 2) : ch0) * 16;
+  const uint32_t sdst = (lane < 4 ? C::oSk : C::oSv) + (lane & 3) * 16;
+  const uint8_t* const ksrc = a.k4 + lane * 16;
+  const uint8_t* const vsrc = a.v4 + lane * 16;
+  const float* const ssrc = (lane < 4 ? a.sk : a.sv) + (lane & 3) * 4;
+  const int32_t* const tb = a.table + static_cast<size_t>(b) * a.max_pages;
+  const int page_mask = (1 << a.page_log2) - 1;
+  // Rows of the cache fit 32 bits: 2^32 rows of 72 bytes and more exceed the memory.
+  const uint32_t page_rows = static_cast<uint32_t>(a.Hk) << a.page_log2, head_row = static_cast<uint32_t>(hk) << a.page_log2;
   auto load = [&](int t, int stage) {
-    uint8_t* const st = ring + stage * C::kStage;
-    const int32_t* const tb = a.table + static_cast<size_t>(b) * a.max_pages;
+    const uint32_t st = ring + stage * C::kStage;
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
       const int key0 = t * kStep + 16 * s;
       const bool live = t < t1 && key0 < len;
-      size_t row = 0;
-      if (live) {
-        int page = __ldg(tb + (key0 >> a.page_log2));
-        if (page < 0 || page >= a.num_pages) {
-          bad |= kStatusBadPosition;
-          page = 0;
-        }
-        row = ((static_cast<size_t>(page) * a.Hk + hk) << a.page_log2) + (key0 & ((1 << a.page_log2) - 1));
+      uint32_t page = live ? static_cast<uint32_t>(__ldg(tb + (key0 >> a.page_log2))) : 0u;
+      if (page >= static_cast<uint32_t>(a.num_pages)) {
+        bad |= kStatusBadPosition;
+        page = 0;
       }
+      const uint32_t row = page * page_rows + head_row + (key0 & page_mask);
       const uint32_t bytes = live ? 16u : 0u;  // 0: the place is filled with zeros
+      const uint8_t* const ks = ksrc + static_cast<uint64_t>(row) * C::kRow;
+      const uint8_t* const vs = vsrc + static_cast<uint64_t>(row) * C::kRow;
 #pragma unroll
-      for (int i = 0; i < 16 * C::kChunks / 32; ++i) {
-        const int idx = lane + 32 * i, x = idx / C::kChunks, ch = idx % C::kChunks;
-        cp_async16(st + (16 * s + k_place(x)) * C::kRow + ch * 16, a.k4 + (row + x) * C::kRow + ch * 16, bytes);
-        const int vch = C::kChunks == 4 ? ch ^ (x & 2) : ch;
-        cp_async16(st + C::oV + (16 * s + x) * C::kRow + vch * 16, a.v4 + (row + x) * C::kRow + ch * 16, bytes);
+      for (int i = 0; i < kCopies; ++i) {
+        cp_async16(st + kdst + (16 * s + 8 * i) * C::kRow, ks + 512 * i, bytes);
+        cp_async16(st + vdst + (16 * s + 8 * i) * C::kRow, vs + 512 * i, bytes);
       }
-      if (lane < 8) {
-        const float* const src = lane < 4 ? a.sk : a.sv;
-        cp_async16(st + (lane < 4 ? C::oSk : C::oSv) + 64 * s + (lane & 3) * 16, src + row + (lane & 3) * 4, bytes);
-      }
+      if (lane < 8) cp_async16(st + sdst + 64 * s, ssrc + row, bytes);
     }
     cp_async_commit();
   };
@@ -254,44 +262,55 @@ __global__ void __launch_bounds__(kRowWarps * 32) kv4_rows_kernel(const RowsArgs
 
   // Q fragments: row 8j + g, the channels of this lane's words.
   uint32_t qf[NT][2 * kW][2];
-  float qscale[NT][2];  // of rows 8j + 2 q4 + {0, 1}: what the scores are multiplied with
-  int lim[NT][2];
-  int lim_min = len;
+  uint4 qraw[NT][kW];
+  float most = 0.0f;
 #pragma unroll
   for (int j = 0; j < NT; ++j) {
     const int r = r0 + 8 * j + g;
     const bool in_use = r < R && r % a.Nq < ql;
     const __nv_bfloat16* const src = a.q + (static_cast<size_t>(bh) * R + (in_use ? r : 0)) * D + q4 * (D / 4);
-    uint4 u[kW];
-    float most = 0.0f;
 #pragma unroll
     for (int w = 0; w < kW; ++w) {
-      u[w] = in_use ? __ldg(reinterpret_cast<const uint4*>(src + 8 * w)) : make_uint4(0, 0, 0, 0);
-      const uint32_t x[4] = {u[w].x, u[w].y, u[w].z, u[w].w};
+      qraw[j][w] = in_use ? __ldg(reinterpret_cast<const uint4*>(src + 8 * w)) : make_uint4(0, 0, 0, 0);
+      const uint32_t x[4] = {qraw[j][w].x, qraw[j][w].y, qraw[j][w].z, qraw[j][w].w};
 #pragma unroll
       for (int i = 0; i < 4; ++i)
         most = fmaxf(most, fmaxf(fabsf(__uint_as_float(x[i] << 16)), fabsf(__uint_as_float(x[i] & 0xFFFF0000u))));
     }
-    most = fmaxf(most, __shfl_xor_sync(0xFFFFFFFFu, most, 1));
-    most = fmaxf(most, __shfl_xor_sync(0xFFFFFFFFu, most, 2));
-    // 2^(14 - exponent of the row's largest value), within what has a normal inverse
-    const int ex = max(static_cast<int>(__float_as_uint(most) >> 23), 15);
-    const float up = __uint_as_float(static_cast<uint32_t>(min(127 + 14 - (ex - 127), 253)) << 23);
+  }
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) most = fmaxf(most, __shfl_xor_sync(0xFFFFFFFFu, most, o));
+  // 2^(14 - exponent of the largest value), within what has a normal inverse
+  const int ex = max(static_cast<int>(__float_as_uint(most) >> 23), 15);
+  const float q_up = __uint_as_float(static_cast<uint32_t>(min(268 - ex, 253)) << 23);
+  const float q_down = a.scale_log2 / q_up * 16777216.0f;  // the scores are multiplied with it
+  float q_off[NT][2];
+  int lim[NT][2];
+  int lim_min = len;
+#pragma unroll
+  for (int j = 0; j < NT; ++j) {
+    float sum = 0.0f;
     auto pair = [&](uint32_t lo, uint32_t hi, bool odd) {  // channels c and c + 4
       const float x = __uint_as_float(odd ? lo & 0xFFFF0000u : lo << 16);
       const float y = __uint_as_float(odd ? hi & 0xFFFF0000u : hi << 16);
+      sum += x + y;
+      const float up = odd ? q_up * 0.0625f : q_up;  // the odd channels' codes come times 16
       return pack_f16(x * up, y * up);
     };
 #pragma unroll
     for (int w = 0; w < kW; ++w) {
-      qf[j][2 * w][0] = pair(u[w].x, u[w].z, false);      // channels 0, 4
-      qf[j][2 * w][1] = pair(u[w].x, u[w].z, true);       // 1, 5
-      qf[j][2 * w + 1][0] = pair(u[w].y, u[w].w, false);  // 2, 6
-      qf[j][2 * w + 1][1] = pair(u[w].y, u[w].w, true);   // 3, 7
+      const uint4 u = qraw[j][w];
+      qf[j][2 * w][0] = pair(u.x, u.z, false);      // channels 0, 4
+      qf[j][2 * w][1] = pair(u.x, u.z, true);       // 1, 5
+      qf[j][2 * w + 1][0] = pair(u.y, u.w, false);  // 2, 6
+      qf[j][2 * w + 1][1] = pair(u.y, u.w, true);   // 3, 7
     }
-    const float down = a.scale_log2 / up;
+    // The codes come as 2^-24 (code + 8): what the 8 adds is known beforehand.
+    sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 1);
+    sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 2);
+    sum *= -8.0f * q_up * 5.9604645e-8f;
 #pragma unroll
-    for (int e = 0; e < 2; ++e) qscale[j][e] = __shfl_sync(0xFFFFFFFFu, down, (2 * q4 + e) * 4);
+    for (int e = 0; e < 2; ++e) q_off[j][e] = __shfl_sync(0xFFFFFFFFu, sum, (2 * q4 + e) * 4);
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
       const int rr = r0 + 8 * j + 2 * q4 + e, i = rr % a.Nq;
@@ -302,14 +321,14 @@ __global__ void __launch_bounds__(kRowWarps * 32) kv4_rows_kernel(const RowsArgs
 
   float acc[NT][kM][4];
   float m[NT][2], l[NT][2];
-  float vref = 9.8607613e-32f;  // 2^-103
+  float vref = 9.8607613e-32f, vinv = kPUp / vref;  // from 2^-103
 #pragma unroll
   for (int j = 0; j < NT; ++j) {
 #pragma unroll
     for (int i = 0; i < kM; ++i)
 #pragma unroll
       for (int e = 0; e < 4; ++e) acc[j][i][e] = 0.0f;
-    m[j][0] = m[j][1] = -INFINITY;
+    m[j][0] = m[j][1] = kNone;
     l[j][0] = l[j][1] = 0.0f;
   }
   int stage = 0;
@@ -321,7 +340,7 @@ __global__ void __launch_bounds__(kRowWarps * 32) kv4_rows_kernel(const RowsArgs
       if (ns >= kStages) ns -= kStages;
       load(t + (kStages - 1) * kRowWarps, ns);
     }
-    const uint8_t* const st = ring + stage * C::kStage;
+    const uint8_t* const st = smem + (warp * kStages + stage) * C::kStage;
     if (++stage == kStages) stage = 0;
     // ---- S^T of 2 x 16 keys
     float s[NT][2][4];
@@ -331,66 +350,97 @@ __global__ void __launch_bounds__(kRowWarps * 32) kv4_rows_kernel(const RowsArgs
       load_words<kW>(st + (16 * u + g) * C::kRow + q4 * (C::kRow / 4), w0);
       load_words<kW>(st + (16 * u + 8 + g) * C::kRow + q4 * (C::kRow / 4), w1);
 #pragma unroll
-      for (int j = 0; j < NT; ++j) s[j][u][0] = s[j][u][1] = s[j][u][2] = s[j][u][3] = 0.0f;
+      for (int j = 0; j < NT; ++j) {
+        s[j][u][0] = s[j][u][2] = q_off[j][0];
+        s[j][u][1] = s[j][u][3] = q_off[j][1];
+      }
 #pragma unroll
       for (int w = 0; w < kW; ++w)
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
           uint32_t af[4];
-          af[0] = codes_f16_lo(w0[w] >> (8 * k));
-          af[1] = codes_f16_lo(w1[w] >> (8 * k));
-          af[2] = codes_f16_hi(w0[w] >> (8 * k));
-          af[3] = codes_f16_hi(w1[w] >> (8 * k));
+          af[0] = raw_f16_lo(w0[w] >> (8 * k));
+          af[1] = raw_f16_lo(w1[w] >> (8 * k));
+          af[2] = raw_f16_hi(w0[w] >> (8 * k));
+          af[3] = raw_f16_hi(w1[w] >> (8 * k));
 #pragma unroll
           for (int j = 0; j < NT; ++j) mma_f16(s[j][u], af, qf[j][2 * w + k][0], qf[j][2 * w + k][1]);
         }
     }
-    // ---- scores in powers of two, masked; the reference maximum
-    const float* const skp = reinterpret_cast<const float*>(st + C::oSk) + key_of(g);
-    const float* const svp = reinterpret_cast<const float*>(st + C::oSv) + key_of(g);
-    const int kbase = t * kStep + key_of(g);
-    const bool edge = t * kStep + kStep > lim_min;
-    bool up = false;
-    float fv[2][2];  // the values' scales; slots behind the last key may hold anything: 0 * NaN is not 0
+    // ---- the keys' and values' scales; masks where a row or the sequence ends in this step
+    float fk[2][2], fv[2][2];
 #pragma unroll
     for (int u = 0; u < 2; ++u)
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        fv[u][e] = kbase + 16 * u + 8 * e < len ? svp[16 * u + 8 * e] : 0.0f;
-        up |= fv[u][e] > vref;
-        const float f = skp[16 * u + 8 * e];
-        const int key = kbase + 16 * u + 8 * e;
-#pragma unroll
-        for (int j = 0; j < NT; ++j)
-#pragma unroll
-          for (int n = 0; n < 2; ++n) {
-            float& y = s[j][u][2 * e + n];
-            y *= f * qscale[j][n];
-            if (edge && key >= lim[j][n]) y = -INFINITY;
-            up |= y > m[j][n] + kLazy;
-          }
+        fk[u][e] = *reinterpret_cast<const float*>(st + C::oSk + (16 * u + 8 * e) * 4 + key_of(g) * 4) * q_down;
+        fv[u][e] = *reinterpret_cast<const float*>(st + C::oSv + (16 * u + 8 * e) * 4 + key_of(g) * 4);
       }
-    if (__any_sync(0xFFFFFFFFu, up)) {
+    if (t * kStep + kStep > lim_min) {
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int key = t * kStep + key_of(g) + 16 * u + 8 * e;
+          if (key >= len) {  // slots behind the last key may hold anything: 0 * NaN is not 0
+            fk[u][e] = 1.0f;
+            fv[u][e] = 0.0f;
+          }
+#pragma unroll
+          for (int j = 0; j < NT; ++j)
+#pragma unroll
+            for (int n = 0; n < 2; ++n)
+              if (key >= lim[j][n]) s[j][u][2 * e + n] = -INFINITY;
+        }
+      // a scale of zero would make NaN of the mask
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) fk[u][e] = fmaxf(fk[u][e], 1e-38f);
+    }
+    // ---- scores beside the reference, in powers of two
+    float z[NT][2][4];
+    float over = fmaxf(fmaxf(fv[0][0], fv[0][1]), fmaxf(fv[1][0], fv[1][1])) > vref ? 1e30f : 0.0f;
+#pragma unroll
+    for (int j = 0; j < NT; ++j)
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+#pragma unroll
+          for (int n = 0; n < 2; ++n) z[j][u][2 * e + n] = fmaf(s[j][u][2 * e + n], fk[u][e], -m[j][n]);
+          over = fmaxf(over, fmaxf(z[j][u][2 * e], z[j][u][2 * e + 1]));
+        }
+    if (__any_sync(0xFFFFFFFFu, over > kLazy)) {
       float v = fmaxf(fmaxf(fv[0][0], fv[0][1]), fmaxf(fv[1][0], fv[1][1]));
 #pragma unroll
       for (int o = 4; o < 32; o <<= 1) v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, o));
       v = fmaxf(vref, __uint_as_float((__float_as_uint(v) + 0x007FFFFFu) & 0x7F800000u));  // a power of two
       const float fr = vref / v;
       vref = v;
+      vinv = kPUp / v;
 #pragma unroll
       for (int j = 0; j < NT; ++j) {
         float f[2];
 #pragma unroll
         for (int n = 0; n < 2; ++n) {
-          float x = fmaxf(fmaxf(s[j][0][n], s[j][0][2 + n]), fmaxf(s[j][1][n], s[j][1][2 + n]));
+          float x = kNone;
+#pragma unroll
+          for (int u = 0; u < 2; ++u) x = fmaxf(x, fmaxf(s[j][u][n] * fk[u][0], s[j][u][2 + n] * fk[u][1]));
 #pragma unroll
           for (int o = 4; o < 32; o <<= 1) x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, o));
           const float mn = fmaxf(m[j][n], x);
-          f[n] = mn == -INFINITY ? 1.0f : ex2_approx(m[j][n] - mn);
+          f[n] = ex2_approx(m[j][n] - mn);
           m[j][n] = mn;
           l[j][n] *= f[n];
           f[n] *= fr;
         }
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+          for (int e = 0; e < 2; ++e)
+#pragma unroll
+            for (int n = 0; n < 2; ++n) z[j][u][2 * e + n] = fmaf(s[j][u][2 * e + n], fk[u][e], -m[j][n]);
 #pragma unroll
         for (int i = 0; i < kM; ++i) {
           acc[j][i][0] *= f[0];
@@ -401,7 +451,6 @@ __global__ void __launch_bounds__(kRowWarps * 32) kv4_rows_kernel(const RowsArgs
       }
     }
     // ---- P^T (times the values' scales) and O^T
-    const float vinv = kPUp / vref;
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
       uint32_t pb[NT][2];
@@ -410,14 +459,10 @@ __global__ void __launch_bounds__(kRowWarps * 32) kv4_rows_kernel(const RowsArgs
         const float fr = fv[u][e] * vinv;
 #pragma unroll
         for (int j = 0; j < NT; ++j) {
-          float p[2];
-#pragma unroll
-          for (int n = 0; n < 2; ++n) {
-            const float mr = m[j][n] == -INFINITY ? 0.0f : m[j][n];
-            p[n] = ex2_approx(s[j][u][2 * e + n] - mr);
-            l[j][n] += p[n];
-          }
-          pb[j][e] = transpose8(pack_f16(p[0] * fr, p[1] * fr));
+          const float p0 = ex2_approx(z[j][u][2 * e]), p1 = ex2_approx(z[j][u][2 * e + 1]);
+          l[j][0] += p0;
+          l[j][1] += p1;
+          pb[j][e] = transpose8(pack_f16(p0 * fr, p1 * fr));
         }
       }
       constexpr int kVW = D / 64;  // code words of a key per lane (V)
@@ -482,7 +527,7 @@ __global__ void __launch_bounds__(kRowWarps * 32) kv4_rows_kernel(const RowsArgs
     const int row = idx / (D / 4), c = (idx % (D / 4)) * 4;
     const int r = r0 + row;
     if (r >= R || r % a.Nq >= ql) continue;
-    float top = -INFINITY;
+    float top = kNone;
 #pragma unroll
     for (int w = 0; w < kRowWarps; ++w) top = fmaxf(top, rm[w * kRows + row]);
     float sum = 0.0f;
@@ -490,13 +535,13 @@ __global__ void __launch_bounds__(kRowWarps * 32) kv4_rows_kernel(const RowsArgs
 #pragma unroll
     for (int w = 0; w < kRowWarps; ++w) {
       const float mw = rm[w * kRows + row];
-      const float f = mw == -INFINITY ? 0.0f : ex2_approx(mw - top);
+      const float f = mw == kNone ? 0.0f : ex2_approx(mw - top);
       const float4 v = *reinterpret_cast<const float4*>(ro + (w * kRows + row) * D + c);
       sum = fmaf(f, rl[w * kRows + row], sum);
       o.x = fmaf(f, v.x, o.x); o.y = fmaf(f, v.y, o.y); o.z = fmaf(f, v.z, o.z); o.w = fmaf(f, v.w, o.w);
     }
-    const float inv = top == -INFINITY ? 0.0f : 1.0f / sum;
-    const float lse2 = top == -INFINITY ? -INFINITY : top + log2f(sum);
+    const float inv = top == kNone ? 0.0f : 1.0f / sum;
+    const float lse2 = top == kNone ? -INFINITY : top + log2f(sum);
     const size_t at = static_cast<size_t>(bh) * R + r;
     o.x *= inv; o.y *= inv; o.z *= inv; o.w *= inv;
     if (a.nsplit == 1) {

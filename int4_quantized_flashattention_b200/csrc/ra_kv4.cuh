@@ -32,19 +32,31 @@ __device__ __forceinline__ uint32_t codes_bf16(uint32_t w) {
   return *reinterpret_cast<const uint32_t*>(&r);
 }
 
+// (a & b) ^ c
+__device__ __forceinline__ uint32_t and_xor(uint32_t a, uint32_t b, uint32_t c) {
+  uint32_t d;
+  asm("lop3.b32 %0, %1, %2, %3, 0x6A;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
+  return d;
+}
+
+// The codes of bits 0-3 and 16-19 (or 4-7 and 20-23) as f16 pairs of 2^-24 (code + 8)
+// (or 2^-20): f16's subnormals are its integers, so the mask alone makes them.
+__device__ __forceinline__ uint32_t raw_f16_lo(uint32_t w) { return and_xor(w, 0x000F000Fu, 0x00080008u); }
+__device__ __forceinline__ uint32_t raw_f16_hi(uint32_t w) { return and_xor(w, 0x00F000F0u, 0x00800080u); }
+
 // The same as f16 pairs, from bits 0-3 and 16-19, and from bits 4-7 and 20-23: f16
 // has ten mantissa bits, so the second pair needs no shift (1024 + 16 (code + 8),
 // times 1/16 and minus 72 in one exact fused operation).  Shifts and masks are what
 // bounds the kernels that unpack in registers: a word takes five of them, in bf16
 // seven.
 __device__ __forceinline__ uint32_t codes_f16_lo(uint32_t w) {
-  const uint32_t x = (w & 0x000F000Fu) ^ 0x64086408u;
+  const uint32_t x = and_xor(w, 0x000F000Fu, 0x64086408u);
   const uint32_t k1032 = 0x64086408u;
   const __half2 r = __hsub2(*reinterpret_cast<const __half2*>(&x), *reinterpret_cast<const __half2*>(&k1032));
   return *reinterpret_cast<const uint32_t*>(&r);
 }
 __device__ __forceinline__ uint32_t codes_f16_hi(uint32_t w) {
-  const uint32_t x = (w & 0x00F000F0u) ^ 0x64806480u;
+  const uint32_t x = and_xor(w, 0x00F000F0u, 0x64806480u);
   const uint32_t k16th = 0x2C002C00u, k72 = 0xD480D480u;  // 1/16 and -72, twice
   const __half2 r = __hfma2(*reinterpret_cast<const __half2*>(&x), *reinterpret_cast<const __half2*>(&k16th),
                             *reinterpret_cast<const __half2*>(&k72));
@@ -91,8 +103,8 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
 }
 
 // 16 bytes global -> shared without registers; `bytes` 0 fills with zeros.
-__device__ __forceinline__ void cp_async16(void* dst, const void* src, uint32_t bytes) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(bytes) : "memory");
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32_t bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
