@@ -359,15 +359,16 @@ ra_status ra_rope_table(const ra_problem* p, void* table, size_t bytes, void* st
  *                q_out may both be NULL (keys only), or k and k_out.
  *   *_weight     fp32 [D], NULL for ones;  *_bias  fp32 [D], NULL for zeros.
  *   pos, table   [N, 3] int32 positions and the table of ra_rope_table for the
- *                same p.  Both NULL: the norm alone, without RoPE and rotation.
+ *                same p (table_bytes at least ra_rope_table_bytes(p)).  Both
+ *                NULL: the norm alone, without RoPE and rotation.
  *   q_out, k_out bf16 [B, H, N, D] and [B, Hk, N, D], dense.  They must not
  *                overlap the inputs.
  */
 ra_status ra_qk_norm_rope(const ra_problem* p, int Hk, int norm, float eps, int in_dtype,
                           const void* q, const ra_strides* q_st, const void* k, const ra_strides* k_st,
                           const float* q_weight, const float* k_weight, const float* q_bias,
-                          const float* k_bias, const int32_t* pos, const void* table, void* q_out,
-                          void* k_out, void* stream);
+                          const float* k_bias, const int32_t* pos, const void* table, size_t table_bytes,
+                          void* q_out, void* k_out, void* stream);
 
 /*
  * A paged cache of keys and values in 4 bits: per token and head the symmetric

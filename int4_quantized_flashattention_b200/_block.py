@@ -11,7 +11,7 @@ from typing import Optional, Tuple
 
 import torch
 
-from . import Problem, _check, _in_dtype, lib
+from . import Problem, _check, lib
 
 NORM_RMS, NORM_LAYER = 0, 1                   # ra_norm_mode
 
@@ -45,7 +45,7 @@ def declare(L) -> None:
     L.ra_rope_table_bytes.restype = sz
     L.ra_rope_table_bytes.argtypes = [P]
     L.ra_rope_table.argtypes = [P, vp, sz, vp]
-    L.ra_qk_norm_rope.argtypes = [P, i, i, C.c_float, i] + [vp] * 13
+    L.ra_qk_norm_rope.argtypes = [P, i, i, C.c_float, i] + [vp] * 10 + [sz] + [vp] * 3
     L.ra_kv4_append.argtypes = [vp, i, i, i] + [vp] * 5 + [i] + [vp] * 3
     L.ra_kv4_read.argtypes = [vp, i, i, i, vp, i] + [vp] * 5
     L.ra_attn_kv4_workspace_bytes.restype = sz
@@ -56,47 +56,63 @@ def declare(L) -> None:
         getattr(L, name).restype = i
 
 
-_SAME = contextlib.nullcontext()
+# The wrappers are most of a small call's time, so they ask for as little as they can: the raw handle of the current
+# stream and the current device's index come from torch's C module, without the objects around them.
+_raw_stream = torch._C._cuda_getCurrentRawStream
+_device = torch._C._cuda_getDevice
+_F32, _BF16, _I32, _U8 = torch.float32, torch.bfloat16, torch.int32, torch.uint8
+_DT = {_F32: 0, _BF16: 1}                     # ra_dtype
 
 
-def _on(dev: torch.device, stream):
-    """Context in which `dev` is the current device and `stream`, if given, the current stream."""
-    if stream is not None:
-        if not hasattr(stream, "cuda_stream"):
-            stream = torch.cuda.ExternalStream(int(stream), device=dev)
-        return torch.cuda.stream(stream)
-    return _SAME if dev.index == torch.cuda.current_device() else torch.cuda.device(dev)
+@contextlib.contextmanager
+def _on(idx: int, stream):
+    """Device `idx` as the current device and `stream` (a stream or its handle), if given, as the current stream."""
+    with torch.cuda.device(idx):
+        if stream is None:
+            yield
+        else:
+            if not hasattr(stream, "cuda_stream"):
+                stream = torch.cuda.ExternalStream(int(stream), device=idx)
+            with torch.cuda.stream(stream):
+                yield
 
 
-def _current() -> int:
-    return torch.cuda.current_stream().cuda_stream
+def _bad(t, dtype, shape, idx, name: str):
+    return ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on CUDA device {idx}, got "
+                      f"{t.dtype}, {tuple(t.shape)}, strides {t.stride()} on {t.device}")
 
 
-def _arg(t: Optional[torch.Tensor], dtype, shape, dev, name: str) -> Optional[int]:
-    """Address of a contiguous tensor of the given dtype and shape on `dev`; None for None."""
+def _arg(t: Optional[torch.Tensor], dtype, shape, idx: int, name: str) -> Optional[int]:
+    """Address of a contiguous tensor of the given dtype and shape on device `idx`; None for None."""
     if t is None:
         return None
-    if t.dtype != dtype or t.shape != shape or t.device != dev or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {dev}, got "
-                         f"{t.dtype}, {tuple(t.shape)}, strides {t.stride()} on {t.device}")
-    return t.data_ptr()
+    if t.dtype is dtype and t.shape == shape and t.get_device() == idx and t.is_contiguous():
+        return t.data_ptr()
+    raise _bad(t, dtype, shape, idx, name)
 
 
-def _view(t: torch.Tensor, dtype, shape, dev, name: str):
-    """Address and Strides of a [B, H, N, D] tensor with contiguous channels."""
-    if t.dtype != dtype or t.shape != shape or t.device != dev:
-        raise ValueError(f"{name} must be a {dtype} tensor of shape {tuple(shape)} on {dev}, got {t.dtype}, "
-                         f"{tuple(t.shape)} on {t.device}")
-    b, h, n, d = t.stride()
-    if d != 1:
+def _view(t: torch.Tensor, dtype, shape, idx: int, name: str):
+    """Address and Strides reference of a [B, H, N, D] tensor with contiguous channels."""
+    if t.dtype is dtype and t.shape == shape and t.get_device() == idx:
+        b, h, n, d = t.stride()
+        if d == 1:
+            return t.data_ptr(), C.byref(Strides(b, h, n))
         raise ValueError(f"{name} must have contiguous channels, got strides {t.stride()}")
-    return t.data_ptr(), Strides(b, h, n)
+    raise ValueError(f"{name} must be a {dtype} tensor of shape {tuple(shape)} on CUDA device {idx}, got {t.dtype}, "
+                     f"{tuple(t.shape)} on {t.device}")
 
 
-def _cuda4(t: torch.Tensor, name: str) -> torch.device:
-    if not t.is_cuda or t.dim() != 4:
+def _cuda4(t: torch.Tensor, name: str) -> int:
+    if t.dim() != 4 or not t.is_cuda:
         raise ValueError(f"{name} must be a four-dimensional CUDA tensor")
-    return t.device
+    return t.get_device()
+
+
+def _dtype(t: torch.Tensor) -> int:
+    try:
+        return _DT[t.dtype]
+    except KeyError:
+        raise ValueError("inputs must be bfloat16 or float32") from None
 
 
 def rope_table(p: Problem, device="cuda", stream=None) -> torch.Tensor:
@@ -104,10 +120,10 @@ def rope_table(p: Problem, device="cuda", stream=None) -> torch.Tensor:
     n = int(lib().ra_rope_table_bytes(C.byref(p)))
     if n == 0:
         raise ValueError("invalid problem")
-    dev = torch.empty(0, device=device).device
-    with _on(dev, stream):
-        t = torch.empty(n // 8, 2, dtype=torch.float32, device=dev)
-        _check("ra_rope_table", lib().ra_rope_table(C.byref(p), t.data_ptr(), n, _current()))
+    idx = torch.empty(0, device=device).get_device()
+    with _on(idx, stream):
+        t = torch.empty(n // 8, 2, dtype=_F32, device="cuda")
+        _check("ra_rope_table", lib().ra_rope_table(C.byref(p), t.data_ptr(), n, _raw_stream(idx)))
     return t
 
 
@@ -123,36 +139,44 @@ def qk_norm_rope(p: Problem, q: Optional[torch.Tensor], k: Optional[torch.Tensor
     some = q if q is not None else k
     if some is None:
         raise ValueError("q or k must be given")
-    dev, dt = _cuda4(some, "q" if q is not None else "k"), some.dtype
-    L, D = lib(), p.D
-    Hk = k.shape[1] if k is not None and k.dim() == 4 else p.H
-    qs, ks = (p.B, p.H, p.N, D), (p.B, Hk, p.N, D)
-    qp = qst = kp = kst = None
+    idx = _cuda4(some, "q" if q is not None else "k")
+    if stream is not None or idx != _device():
+        with _on(idx, stream):
+            return qk_norm_rope(p, q, k, table, pos, q_weight, k_weight, q_bias, k_bias, norm, eps, q_out, k_out)
+    B, H, N, D = p.B, p.H, p.N, p.D
+    dt = some.dtype
+    Hk = H
+    qp = qs = qo = kp = ks = ko = None
     if q is not None:
-        qp, qst = _view(q, dt, qs, dev, "q")
-        qst = C.byref(qst)
+        shape = (B, H, N, D)
+        qp, qs = _view(q, dt, shape, idx, "q")
+        if q_out is None:
+            q_out = torch.empty(shape, dtype=_BF16, device=q.device)
+            qo = q_out.data_ptr()
+        else:
+            qo = _arg(q_out, _BF16, shape, idx, "q_out")
+    else:
+        q_out = None
     if k is not None:
-        kp, kst = _view(k, dt, ks, dev, "k")
-        kst = C.byref(kst)
-    if table is not None and 8 * table.shape[0] < L.ra_rope_table_bytes(C.byref(p)):
-        raise ValueError("table is shorter than the RoPE table of p")
-    f32, bf16 = torch.float32, torch.bfloat16
-    with _on(dev, stream):
-        if q is None:
-            q_out = None
-        elif q_out is None:
-            q_out = torch.empty(qs, dtype=bf16, device=dev)
-        if k is None:
-            k_out = None
-        elif k_out is None:
-            k_out = torch.empty(ks, dtype=bf16, device=dev)
-        _check("ra_qk_norm_rope", L.ra_qk_norm_rope(
-            C.byref(p), Hk, norm, eps, _in_dtype(some), qp, qst, kp, kst,
-            _arg(q_weight, f32, (D,), dev, "q_weight"), _arg(k_weight, f32, (D,), dev, "k_weight"),
-            _arg(q_bias, f32, (D,), dev, "q_bias"), _arg(k_bias, f32, (D,), dev, "k_bias"),
-            _arg(pos, torch.int32, (p.N, 3), dev, "pos"),
-            None if table is None else _arg(table, f32, (table.shape[0], 2), dev, "table"),
-            _arg(q_out, bf16, qs, dev, "q_out"), _arg(k_out, bf16, ks, dev, "k_out"), _current()))
+        Hk = k.shape[1] if k.dim() == 4 else H
+        shape = (B, Hk, N, D)
+        kp, ks = _view(k, dt, shape, idx, "k")
+        if k_out is None:
+            k_out = torch.empty(shape, dtype=_BF16, device=k.device)
+            ko = k_out.data_ptr()
+        else:
+            ko = _arg(k_out, _BF16, shape, idx, "k_out")
+    else:
+        k_out = None
+    w = (D,)
+    rc = lib().ra_qk_norm_rope(
+        C.byref(p), Hk, norm, eps, _dtype(some), qp, qs, kp, ks, _arg(q_weight, _F32, w, idx, "q_weight"),
+        _arg(k_weight, _F32, w, idx, "k_weight"), _arg(q_bias, _F32, w, idx, "q_bias"),
+        _arg(k_bias, _F32, w, idx, "k_bias"), _arg(pos, _I32, (N, 3), idx, "pos"),
+        None if table is None else _arg(table, _F32, (len(table), 2), idx, "table"),
+        0 if table is None else 8 * len(table), qo, ko, _raw_stream(idx))
+    if rc:
+        _check("ra_qk_norm_rope", rc)
     return q_out, k_out
 
 
@@ -161,65 +185,76 @@ class KV4Cache:
     sk, sv [num_pages, Hk, page_size] fp32.  Only a handle: the tensors are the caller's, kept alive by it."""
 
     def __init__(self, k4: torch.Tensor, sk: torch.Tensor, v4: torch.Tensor, sv: torch.Tensor):
-        dev = _cuda4(k4, "k4")
-        n, hk, page, half = k4.shape
-        self.k4, self.sk, self.v4, self.sv, self.device = k4, sk, v4, sv, dev
+        idx = _cuda4(k4, "k4")
+        codes = k4.shape
+        n, hk, page, half = codes
+        scales = codes[:3]
+        self.k4, self.sk, self.v4, self.sv, self.index = k4, sk, v4, sv, idx
         self.num_pages, self.Hk, self.page_size, self.D = n, hk, page, 2 * half
-        codes, scales = (n, hk, page, half), (n, hk, page)
-        self._c = _Kv4Cache(n, page, hk, 2 * half, _arg(k4, torch.uint8, codes, dev, "k4"),
-                            _arg(sk, torch.float32, scales, dev, "sk"), _arg(v4, torch.uint8, codes, dev, "v4"),
-                            _arg(sv, torch.float32, scales, dev, "sv"))
+        self._c = _Kv4Cache(n, page, hk, 2 * half, _arg(k4, _U8, codes, idx, "k4"), _arg(sk, _F32, scales, idx, "sk"),
+                            _arg(v4, _U8, codes, idx, "v4"), _arg(sv, _F32, scales, idx, "sv"))
         self._ref = C.byref(self._c)
 
     @classmethod
     def empty(cls, num_pages: int, page_size: int, Hk: int, D: int, device="cuda") -> "KV4Cache":
         """A cache of zeros."""
         def codes():
-            return torch.zeros(num_pages, Hk, page_size, D // 2, dtype=torch.uint8, device=device)
+            return torch.zeros(num_pages, Hk, page_size, D // 2, dtype=_U8, device=device)
 
         def scales():
-            return torch.zeros(num_pages, Hk, page_size, dtype=torch.float32, device=device)
+            return torch.zeros(num_pages, Hk, page_size, dtype=_F32, device=device)
         return cls(codes(), scales(), codes(), scales())
 
 
 def _table(cache: KV4Cache, t: torch.Tensor, B: int) -> int:
     if t.dim() != 2:
         raise ValueError("block_table must be [B, max_pages]")
-    return _arg(t, torch.int32, (B, t.shape[1]), cache.device, "block_table")
+    return _arg(t, _I32, (B, t.shape[1]), cache.index, "block_table")
 
 
 def kv4_append(cache: KV4Cache, k: torch.Tensor, v: torch.Tensor, block_table: torch.Tensor,
                start: Optional[torch.Tensor] = None, n_new: Optional[torch.Tensor] = None, stream=None) -> None:
     """ra_kv4_append: quantises k, v [B, Hk, T, D] (any strides with contiguous channels) into the cache at
     positions start[b] + 0 .. n_new[b] - 1 of each sequence."""
-    dev = cache.device
+    idx = cache.index
+    if stream is not None or idx != _device():
+        with _on(idx, stream):
+            return kv4_append(cache, k, v, block_table, start, n_new)
     _cuda4(k, "k")
-    B, T = k.shape[0], k.shape[2]
+    B, T, dt = k.shape[0], k.shape[2], k.dtype
     shape = (B, cache.Hk, T, cache.D)
-    kp, ks = _view(k, k.dtype, shape, dev, "k")
-    vp, vs = _view(v, k.dtype, shape, dev, "v")
-    with _on(dev, stream):
-        _check("ra_kv4_append", lib().ra_kv4_append(
-            cache._ref, _in_dtype(k), B, T, kp, C.byref(ks), vp, C.byref(vs), _table(cache, block_table, B),
-            block_table.shape[1], _arg(start, torch.int32, (B,), dev, "start"),
-            _arg(n_new, torch.int32, (B,), dev, "n_new"), _current()))
+    kp, ks = _view(k, dt, shape, idx, "k")
+    vp, vs = _view(v, dt, shape, idx, "v")
+    b = (B,)
+    rc = lib().ra_kv4_append(cache._ref, _dtype(k), B, T, kp, ks, vp, vs, _table(cache, block_table, B),
+                             block_table.shape[1], _arg(start, _I32, b, idx, "start"),
+                             _arg(n_new, _I32, b, idx, "n_new"), _raw_stream(idx))
+    if rc:
+        _check("ra_kv4_append", rc)
 
 
 def kv4_read(cache: KV4Cache, block_table: torch.Tensor, start: Optional[torch.Tensor], T: int,
-             n: Optional[torch.Tensor] = None, dtype: torch.dtype = torch.bfloat16,
+             n: Optional[torch.Tensor] = None, dtype: torch.dtype = _BF16,
              out: Optional[Tuple[torch.Tensor, torch.Tensor]] = None, stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
     """ra_kv4_read: tokens start[b] .. start[b] + n[b] - 1 as code * scale in dense k, v [B, Hk, T, D]; rows at and
     past n[b] are left as they were."""
-    dev, B = cache.device, block_table.shape[0]
+    idx = cache.index
+    if stream is not None or idx != _device():
+        with _on(idx, stream):
+            return kv4_read(cache, block_table, start, T, n, dtype, out)
+    B = block_table.shape[0]
     shape = (B, cache.Hk, T, cache.D)
-    with _on(dev, stream):
-        if out is None:
-            out = (torch.empty(shape, dtype=dtype, device=dev), torch.empty(shape, dtype=dtype, device=dev))
+    if out is None:
+        k, v = torch.empty(shape, dtype=dtype, device=cache.k4.device), torch.empty(shape, dtype=dtype,
+                                                                                  device=cache.k4.device)
+    else:
         k, v = out
-        _check("ra_kv4_read", lib().ra_kv4_read(
-            cache._ref, _in_dtype(k), B, T, _table(cache, block_table, B), block_table.shape[1],
-            _arg(start, torch.int32, (B,), dev, "start"), _arg(n, torch.int32, (B,), dev, "n"),
-            _arg(k, k.dtype, shape, dev, "k"), _arg(v, k.dtype, shape, dev, "v"), _current()))
+    b = (B,)
+    rc = lib().ra_kv4_read(cache._ref, _dtype(k), B, T, _table(cache, block_table, B), block_table.shape[1],
+                           _arg(start, _I32, b, idx, "start"), _arg(n, _I32, b, idx, "n"),
+                           _arg(k, k.dtype, shape, idx, "k"), _arg(v, k.dtype, shape, idx, "v"), _raw_stream(idx))
+    if rc:
+        _check("ra_kv4_read", rc)
     return k, v
 
 
@@ -239,33 +274,39 @@ def attn_kv4(cache: KV4Cache, q: torch.Tensor, block_table: torch.Tensor, seq_le
              workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """ra_attn_kv4: attention of q [B, H, Nq, D] bf16 over the cache; returns out [B, H, Nq, D] bf16.  max_len is a
     bound on seq_lens that the split of the keys is planned for (the block table's reach by default)."""
-    dev = _cuda4(q, "q")
+    idx = _cuda4(q, "q")
+    if stream is not None or idx != _device():
+        with _on(idx, stream):
+            return attn_kv4(cache, q, block_table, seq_lens, q_lens, causal, scale, max_len, out, lse, workspace)
     shape = q.shape
     B, H, Nq, D = shape
-    if dev != cache.device or D != cache.D:
-        raise ValueError(f"q must have {cache.D} channels and be on {cache.device}, got {D} on {dev}")
+    if idx != cache.index or D != cache.D:
+        raise ValueError(f"q must have {cache.D} channels and be on CUDA device {cache.index}, got {D} on {idx}")
     table = _table(cache, block_table, B)
     pages = block_table.shape[1]
     a = C.byref(_Kv4Attn(B, H, Nq, pages, pages * cache.page_size if max_len is None else max_len,
                          1 if causal else 0, _scale(scale, D)))
     L = lib()
-    with _on(dev, stream):
-        if out is None:
-            out = torch.empty(shape, dtype=torch.bfloat16, device=dev)
-        if workspace is None:
-            need = L.ra_attn_kv4_workspace_bytes(cache._ref, a)
-            wp = None
-            if need:
-                workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-                wp = workspace.data_ptr()
-        else:
-            need = workspace.numel()
-            wp = _arg(workspace, torch.uint8, (need,), dev, "workspace")
-        _check("ra_attn_kv4", L.ra_attn_kv4(
-            cache._ref, a, _arg(q, torch.bfloat16, shape, dev, "q"), table,
-            _arg(seq_lens, torch.int32, (B,), dev, "seq_lens"), _arg(q_lens, torch.int32, (B,), dev, "q_lens"),
-            wp, need, _arg(out, torch.bfloat16, shape, dev, "out"),
-            _arg(lse, torch.float32, (B, H, Nq), dev, "lse"), _current()))
+    if out is None:
+        out = torch.empty(shape, dtype=_BF16, device=q.device)
+        op = out.data_ptr()
+    else:
+        op = _arg(out, _BF16, shape, idx, "out")
+    wp = None
+    if workspace is None:
+        need = L.ra_attn_kv4_workspace_bytes(cache._ref, a)
+        if need:
+            workspace = torch.empty(need, dtype=_U8, device=q.device)
+            wp = workspace.data_ptr()
+    else:
+        need = workspace.numel()
+        wp = _arg(workspace, _U8, (need,), idx, "workspace")
+    b = (B,)
+    rc = L.ra_attn_kv4(cache._ref, a, _arg(q, _BF16, shape, idx, "q"), table, _arg(seq_lens, _I32, b, idx, "seq_lens"),
+                       _arg(q_lens, _I32, b, idx, "q_lens"), wp, need, op, _arg(lse, _F32, shape[:3], idx, "lse"),
+                       _raw_stream(idx))
+    if rc:
+        _check("ra_attn_kv4", rc)
     return out
 
 
@@ -274,20 +315,24 @@ def attn_cross(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, kv_lens: Optio
                lse: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """ra_attn_cross: attention of q [B, H, Nq, D] to an encoder's k, v [B, Hk, Nk, D], bf16 with any strides that
     keep the channels contiguous; keys at and past kv_lens[b] take no part.  Returns out, dense unless given."""
-    dev = _cuda4(q, "q")
+    idx = _cuda4(q, "q")
+    if stream is not None or idx != _device():
+        with _on(idx, stream):
+            return attn_cross(q, k, v, kv_lens, scale, out, lse)
     _cuda4(k, "k")
-    bf16, shape = torch.bfloat16, q.shape
+    shape = q.shape
     B, H, Nq, D = shape
     Hk, Nk = k.shape[1], k.shape[2]
-    qp, qs = _view(q, bf16, shape, dev, "q")
-    kp, ks = _view(k, bf16, (B, Hk, Nk, D), dev, "k")
-    vp, vs = _view(v, bf16, (B, Hk, Nk, D), dev, "v")
-    with _on(dev, stream):
-        if out is None:
-            out = torch.empty(shape, dtype=bf16, device=dev)
-        op, os_ = _view(out, bf16, shape, dev, "out")
-        _check("ra_attn_cross", lib().ra_attn_cross(
-            C.byref(_CrossProblem(B, H, Hk, Nq, Nk, D, _scale(scale, D))), qp, C.byref(qs), kp, C.byref(ks), vp,
-            C.byref(vs), _arg(kv_lens, torch.int32, (B,), dev, "kv_lens"), op, C.byref(os_),
-            _arg(lse, torch.float32, (B, H, Nq), dev, "lse"), _current()))
+    kshape = (B, Hk, Nk, D)
+    qp, qs = _view(q, _BF16, shape, idx, "q")
+    kp, ks = _view(k, _BF16, kshape, idx, "k")
+    vp, vs = _view(v, _BF16, kshape, idx, "v")
+    if out is None:
+        out = torch.empty(shape, dtype=_BF16, device=q.device)
+    op, os_ = _view(out, _BF16, shape, idx, "out")
+    rc = lib().ra_attn_cross(C.byref(_CrossProblem(B, H, Hk, Nq, Nk, D, _scale(scale, D))), qp, qs, kp, ks, vp, vs,
+                             _arg(kv_lens, _I32, (B,), idx, "kv_lens"), op, os_,
+                             _arg(lse, _F32, shape[:3], idx, "lse"), _raw_stream(idx))
+    if rc:
+        _check("ra_attn_cross", rc)
     return out

@@ -71,7 +71,7 @@ ra_status ra_rope_table(const ra_problem* p, void* table, size_t bytes, void* st
 ra_status ra_qk_norm_rope(const ra_problem* p, int Hk, int norm, float eps, int in_dtype, const void* q,
                           const ra_strides* q_st, const void* k, const ra_strides* k_st, const float* q_weight,
                           const float* k_weight, const float* q_bias, const float* k_bias, const int32_t* pos,
-                          const void* table, void* q_out, void* k_out, void* stream) {
+                          const void* table, size_t table_bytes, void* q_out, void* k_out, void* stream) {
   if (ra_workspace_bytes(p) == 0 || (in_dtype != RA_DT_F32 && in_dtype != RA_DT_BF16)) return RA_ERR_INVALID_ARG;
   if (norm != RA_NORM_RMS && norm != RA_NORM_LAYER) return RA_ERR_INVALID_ARG;
   if (!(eps >= 0.0f) || !std::isfinite(eps) || Hk < 1) return RA_ERR_INVALID_ARG;
@@ -79,6 +79,7 @@ ra_status ra_qk_norm_rope(const ra_problem* p, int Hk, int norm, float eps, int 
   if (p->B > kMaxGrid || static_cast<int64_t>(p->H) + Hk > kMaxGrid) return RA_ERR_UNSUPPORTED;
   if ((!q) != (!q_out) || (!k) != (!k_out) || (!q && !k)) return RA_ERR_INVALID_ARG;
   if ((!pos) != (!table) || !aligned4_or_null(pos) || !aligned16_or_null(table)) return RA_ERR_INVALID_ARG;
+  if (table && table_bytes < ra_rope_table_bytes(p)) return RA_ERR_INVALID_ARG;
   const int size = in_dtype == RA_DT_BF16 ? 2 : 4;
   ra::NormRopeCall c{};
   const void* x[2] = {q, k};

@@ -235,17 +235,16 @@ __global__ void __launch_bounds__(kRowWarps * 32) kv4_rows_kernel(const RowsArgs
   const uint32_t page_rows = static_cast<uint32_t>(a.Hk) << a.page_log2, head_row = static_cast<uint32_t>(hk) << a.page_log2;
   auto load = [&](int t, int stage) {
     const uint32_t st = ring + stage * C::kStage;
-#pragma unroll
-    for (int s = 0; s < 2; ++s) {
-      const int key0 = t * kStep + 16 * s;
-      const bool live = t < t1 && key0 < len;
-      uint32_t page = live ? static_cast<uint32_t>(__ldg(tb + (key0 >> a.page_log2))) : 0u;
+    const int left = t < t1 ? len - t * kStep : 0;  // keys of this step
+    auto row_of = [&](int key0) -> uint32_t {
+      uint32_t page = static_cast<uint32_t>(__ldg(tb + (key0 >> a.page_log2)));
       if (page >= static_cast<uint32_t>(a.num_pages)) {
         bad |= kStatusBadPosition;
         page = 0;
       }
-      const uint32_t row = page * page_rows + head_row + (key0 & page_mask);
-      const uint32_t bytes = live ? 16u : 0u;  // 0: the place is filled with zeros
+      return page * page_rows + head_row + (key0 & page_mask);
+    };
+    auto copy = [&](int s, uint32_t row, uint32_t bytes) {  // bytes 0: the places are filled with zeros
       const uint8_t* const ks = ksrc + static_cast<uint64_t>(row) * C::kRow;
       const uint8_t* const vs = vsrc + static_cast<uint64_t>(row) * C::kRow;
 #pragma unroll
@@ -254,7 +253,13 @@ __global__ void __launch_bounds__(kRowWarps * 32) kv4_rows_kernel(const RowsArgs
         cp_async16(st + vdst + (16 * s + 8 * i) * C::kRow, vs + 512 * i, bytes);
       }
       if (lane < 8) cp_async16(st + sdst + 64 * s, ssrc + row, bytes);
-    }
+    };
+    const uint32_t row0 = left > 0 ? row_of(t * kStep) : 0u;
+    uint32_t row1 = row0 + 16;  // the same page, but for pages of 16
+    if (left <= 16) row1 = 0;
+    else if (a.page_log2 == 4) row1 = row_of(t * kStep + 16);
+    copy(0, row0, left > 0 ? 16u : 0u);
+    copy(1, row1, left > 16 ? 16u : 0u);
     cp_async_commit();
   };
 #pragma unroll
@@ -400,7 +405,8 @@ __global__ void __launch_bounds__(kRowWarps * 32) kv4_rows_kernel(const RowsArgs
     }
     // ---- scores beside the reference, in powers of two
     float z[NT][2][4];
-    float over = fmaxf(fmaxf(fv[0][0], fv[0][1]), fmaxf(fv[1][0], fv[1][1])) > vref ? 1e30f : 0.0f;
+    const float fv_top = max3(fv[0][0], fv[0][1], fmaxf(fv[1][0], fv[1][1]));
+    float over = fv_top > vref ? 1e30f : 0.0f;
 #pragma unroll
     for (int j = 0; j < NT; ++j)
 #pragma unroll
@@ -409,10 +415,10 @@ __global__ void __launch_bounds__(kRowWarps * 32) kv4_rows_kernel(const RowsArgs
         for (int e = 0; e < 2; ++e) {
 #pragma unroll
           for (int n = 0; n < 2; ++n) z[j][u][2 * e + n] = fmaf(s[j][u][2 * e + n], fk[u][e], -m[j][n]);
-          over = fmaxf(over, fmaxf(z[j][u][2 * e], z[j][u][2 * e + 1]));
+          over = max3(over, z[j][u][2 * e], z[j][u][2 * e + 1]);
         }
     if (__any_sync(0xFFFFFFFFu, over > kLazy)) {
-      float v = fmaxf(fmaxf(fv[0][0], fv[0][1]), fmaxf(fv[1][0], fv[1][1]));
+      float v = fv_top;
 #pragma unroll
       for (int o = 4; o < 32; o <<= 1) v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, o));
       v = fmaxf(vref, __uint_as_float((__float_as_uint(v) + 0x007FFFFFu) & 0x7F800000u));  // a power of two
@@ -491,6 +497,7 @@ __global__ void __launch_bounds__(kRowWarps * 32) kv4_rows_kernel(const RowsArgs
       }
     }
   }
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   cp_async_wait<0>();
   if (bad) atomicOr(&g_kv4_status, bad);
 
@@ -562,6 +569,7 @@ __global__ void __launch_bounds__(128) kv4_join_kernel(Kv4Parts parts, int nspli
   constexpr int kC = D / 32;
   const int lane = threadIdx.x & 31;
   const long long r = static_cast<long long>(blockIdx.x) * 4 + (threadIdx.x >> 5);
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // the parts: this launch may have begun before they end
   if (r >= rows) return;
   if (q_lens && static_cast<int>(r % Nq) >= __ldg(q_lens + r / rows_b)) return;
   float top = -INFINITY;
@@ -656,23 +664,26 @@ Kv4Plan kv4_plan(const ra_kv4_cache& c, const ra_kv4_attn& a) {
   Kv4Plan plan{};
   const long long R = static_cast<long long>(a.H / c.Hk) * a.Nq, bh = static_cast<long long>(a.B) * c.Hk;
   plan.tiles = R > 16;
-  const long long slots = plan.tiles ? kNumSMs : 4 * kNumSMs;
+  // The number of parts with the least estimated time, in keys of work of one SM:
+  // an SM gets the ceiling of its share of CTAs, each of which costs its keys and a
+  // fixed part (kFixed), and joining costs a launch and the parts' traffic.  Few-row
+  // CTAs share an SM, whose rate one or two of them do not reach.  (Measured: 640
+  // heads x 8191 keys 162, 151, 151, 154, 170 us at 1, 2, 3, 5, 9 parts; 8 heads x
+  // 32760 keys 59, 36, 29, 31, 39 us at 4, 9, 18, 28, 64.)
   const long long items = bh * (plan.tiles ? (R + 255) / 256 : 1);
-  const int keys = plan.tiles ? 512 : 128;  // a part has at least this many keys
-  const int most = a.max_len < keys ? 1 : a.max_len / keys;
-  // The smallest number of parts whose last wave of CTAs is nearly full.
-  int best = 1;
-  double best_fill = 0.0;
-  for (int k = 1; k <= most && k <= 64; ++k) {
-    const long long n = items * k;
-    const double fill = static_cast<double>(n) / static_cast<double>((n + slots - 1) / slots * slots);
-    if (fill > best_fill + 0.02) {
-      best = k;
-      best_fill = fill;
+  const double fixed = plan.tiles ? 256.0 : 350.0, join = plan.tiles ? 300.0 : 700.0;
+  const int step = plan.tiles ? 64 : kRowWarps * kStep;
+  double best = 0.0;
+  for (int k = 1; k <= 64 && (k == 1 || (k - 1) * step < a.max_len); ++k) {
+    const long long ctas = (items * k + kNumSMs - 1) / kNumSMs;
+    const double rate = plan.tiles || ctas >= 3 ? 1.0 : ctas == 2 ? 0.9 : 0.75;
+    double cost = ctas * (a.max_len / static_cast<double>(k) + fixed) / rate;
+    if (k > 1) cost += join + (plan.tiles ? 0.015 : 0.06) * k * static_cast<double>(bh) * R * c.D / 128.0;
+    if (k == 1 || cost < 0.98 * best) {
+      best = cost;
+      plan.nsplit = k;
     }
-    if (fill >= 0.9) break;
   }
-  plan.nsplit = best;
   return plan;
 }
 
@@ -707,11 +718,20 @@ cudaError_t launch_kv4_rows(const ra_kv4_cache& c, const ra_kv4_attn& at, const 
 cudaError_t launch_kv4_join(const ra_kv4_cache& c, const ra_kv4_attn& a, const Kv4Plan& plan,
                             const int32_t* q_lens, const Kv4Parts& parts, void* out, float* lse, cudaStream_t st) {
   const long long rows = static_cast<long long>(a.B) * a.H * a.Nq;
-  const int grid = static_cast<int>((rows + 3) / 4), rows_b = a.H * a.Nq;
+  const int rows_b = a.H * a.Nq;
   __nv_bfloat16* o = static_cast<__nv_bfloat16*>(out);
-  if (c.D == 64) kv4_join_kernel<64><<<grid, 128, 0, st>>>(parts, plan.nsplit, rows, a.Nq, rows_b, q_lens, o, lse);
-  else kv4_join_kernel<128><<<grid, 128, 0, st>>>(parts, plan.nsplit, rows, a.Nq, rows_b, q_lens, o, lse);
-  return cudaGetLastError();
+  cudaLaunchAttribute at;
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>((rows + 3) / 4));
+  cfg.blockDim = dim3(128);
+  cfg.stream = st;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  return c.D == 64
+             ? cudaLaunchKernelEx(&cfg, kv4_join_kernel<64>, parts, plan.nsplit, rows, a.Nq, rows_b, q_lens, o, lse)
+             : cudaLaunchKernelEx(&cfg, kv4_join_kernel<128>, parts, plan.nsplit, rows, a.Nq, rows_b, q_lens, o, lse);
 }
 
 cudaError_t read_kv4_status(uint32_t* out) {

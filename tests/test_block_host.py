@@ -31,11 +31,11 @@ def _st(ra, b, h, n):
 
 
 def _norm(ra, p=None, Hk=4, norm=0, eps=1e-6, dt=1, q=GOOD, qst=None, k=GOOD, kst=None, qw=GOOD, kw=GOOD, qb=None,
-          kb=None, pos=GOOD, table=GOOD, qo=GOOD, ko=GOOD):
+          kb=None, pos=GOOD, table=GOOD, tb=1 << 20, qo=GOOD, ko=GOOD):
     p = p or _problem(ra)
     dense = _st(ra, 4 * 105 * 128, 105 * 128, 128)
     return ra.lib().ra_qk_norm_rope(C.byref(p), Hk, norm, eps, dt, q, C.byref(qst or dense), k, C.byref(kst or dense),
-                                    qw, kw, qb, kb, pos, table, qo, ko, None)
+                                    qw, kw, qb, kb, pos, table, tb, qo, ko, None)
 
 
 def _reaches_launch(rc):
@@ -45,7 +45,7 @@ def _reaches_launch(rc):
 @pytest.mark.parametrize("kw", [
     dict(Hk=0), dict(norm=2), dict(norm=-1), dict(eps=-1.0), dict(eps=float("nan")), dict(dt=2), dict(q=BAD16),
     dict(k=BAD16), dict(q=None), dict(qo=None), dict(ko=None), dict(k=None), dict(pos=None), dict(table=None),
-    dict(table=BAD16), dict(pos=BAD4), dict(qw=BAD4), dict(qo=BAD16), dict(q=None, qo=None, k=None, ko=None),
+    dict(table=BAD16), dict(tb=2543), dict(pos=BAD4), dict(qw=BAD4), dict(qo=BAD16), dict(q=None, qo=None, k=None, ko=None),
     dict(Hk=1 << 20)])
 def test_norm_rope_refusals(ra, kw):
     assert _norm(ra, **kw) in (INVALID, UNSUPPORTED)

@@ -470,7 +470,7 @@ def test_wrappers_refuse(ra, gen):
     with pytest.raises(ValueError):
         ra.kv4_append(c, x.half(), x.half(), table)
     p = ra.Problem.make(1, 2, 64, SEG[64], (5, 1, 1))
-    with pytest.raises(ValueError):
+    with pytest.raises(ra.RaError):
         ra.qk_norm_rope(p, x, x, ra.rope_table(p)[:3], _positions((5, 1, 1), 5))
     with pytest.raises(ra.RaError):
         ra.qk_norm_rope(p, x, x, ra.rope_table(p), None)
