@@ -62,77 +62,84 @@ __device__ __forceinline__ long long token_row(const CacheArgs& a, int t) {
 }
 
 // D/8 lanes per token row, eight channels each; a thread stays with one token
-// and walks over heads, so its page is looked up once.  Bound: HBM.
+// and walks over heads, so its page is looked up once, and the loads of the
+// next heads travel while it works.  Bound: HBM.
 template <bool kBf16, int kD>
 __global__ void __launch_bounds__(kThreads) kv4_append_kernel(const CacheArgs a) {
-  constexpr int kLanes = kD / 8, kTok = 32 / kLanes;
+  constexpr int kLanes = kD / 8, kTok = 32 / kLanes, kAhead = kBf16 ? 4 : 2;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int t = (blockIdx.x * (kThreads / 32) + warp) * kTok + lane / kLanes;
   const int c0 = (lane % kLanes) * 8;
   const int which = static_cast<int>(blockIdx.y) >= a.groups ? 1 : 0;
   const int h0 = (blockIdx.y - (which ? a.groups : 0)) * a.group, h1 = min(h0 + a.group, a.Hk);
   const long long row = token_row(a, t);
+  // Lanes without a row (padding, no place) work on zeros and do not store.
   const size_t src = blockIdx.z * a.st[which].b + static_cast<size_t>(row < 0 ? 0 : t) * a.st[which].n + c0;
-#pragma unroll 4
-  for (int h = h0; h < h1; ++h) {
-    float x[8];
-    if (row >= 0) {
-      Raw8<kBf16> raw;
-      load_raw8<kBf16>(a.x[which], src + h * a.st[which].h, raw);
-      unpack8<kBf16>(raw, x);
-    } else {
+  Raw8<kBf16> next[kAhead];
+  auto load = [&](int h, Raw8<kBf16>& r) {
+    if (h < h1 && row >= 0) load_raw8<kBf16>(a.x[which], src + h * a.st[which].h, r);
+    else r = Raw8<kBf16>{};
+  };
 #pragma unroll
-      for (int i = 0; i < 8; ++i) x[i] = 0.0f;
+  for (int i = 0; i < kAhead; ++i) load(h0 + i, next[i]);
+  for (int hb = h0; hb < h1; hb += kAhead) {
+    Raw8<kBf16> cur[kAhead];
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      cur[i] = next[i];
+      load(hb + kAhead + i, next[i]);
     }
-    float m = 0.0f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(x[i]));
-    m = group_max(m, kLanes);
-    if (m < kKv4Tiny) m = 0.0f;  // 7 / m would leave fp32's range
-    const float inv = m == 0.0f ? 0.0f : __fdiv_rn(7.0f, m);
-    uint32_t bits[8];
+    for (int u = 0; u < kAhead; ++u) {
+      const int h = hb + u;
+      float x[8];
+      unpack8<kBf16>(cur[u], x);
+      float m = 0.0f;
 #pragma unroll
-    for (int i = 0; i < 8; i += 2) quant4_bits2(x[i], x[i + 1], inv, inv, bits + i);
-    if (row >= 0) {
-      const size_t at = static_cast<size_t>(row) + (static_cast<size_t>(h) << a.page_log2);
-      *reinterpret_cast<uint32_t*>(a.codes[which] + at * (kD / 2) + (c0 >> 1)) = pack8_bits(bits);
-      if (c0 == 0) a.scale[which][at] = __fdiv_rn(m, 7.0f);
+      for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(x[i]));
+      m = group_max(m, kLanes);
+      if (m < kKv4Tiny) m = 0.0f;  // 7 / m would leave fp32's range
+      const float inv = m == 0.0f ? 0.0f : __fdiv_rn(7.0f, m);
+      uint32_t bits[8];
+#pragma unroll
+      for (int i = 0; i < 8; i += 2) quant4_bits2(x[i], x[i + 1], inv, inv, bits + i);
+      if (h < h1 && row >= 0) {
+        const size_t at = static_cast<size_t>(row) + (static_cast<size_t>(h) << a.page_log2);
+        *reinterpret_cast<uint32_t*>(a.codes[which] + at * (kD / 2) + (c0 >> 1)) = pack8_bits(bits);
+        if (c0 == 0) a.scale[which][at] = __fdiv_rn(m, 7.0f);
+      }
     }
   }
 }
 
+// The same walk the other way.  A lane writes 16 bytes of a row, so that a
+// warp's stores are whole lines: eight bf16 channels, or four fp32 channels from
+// one half of a code word.
 template <bool kBf16, int kD>
 __global__ void __launch_bounds__(kThreads) kv4_read_kernel(const CacheArgs a) {
-  constexpr int kLanes = kD / 8, kTok = 32 / kLanes;
+  constexpr int kCh = kBf16 ? 8 : 4, kLanes = kD / kCh, kTok = 32 / kLanes;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int t = (blockIdx.x * (kThreads / 32) + warp) * kTok + lane / kLanes;
-  const int c0 = (lane % kLanes) * 8;
+  const int c0 = (lane % kLanes) * kCh;
   const int which = static_cast<int>(blockIdx.y) >= a.groups ? 1 : 0;
   const int h0 = (blockIdx.y - (which ? a.groups : 0)) * a.group, h1 = min(h0 + a.group, a.Hk);
   const long long row = token_row(a, t);
   if (row < 0) return;
-#pragma unroll 4
+#pragma unroll 8
   for (int h = h0; h < h1; ++h) {
     const size_t at = static_cast<size_t>(row) + (static_cast<size_t>(h) << a.page_log2);
-    const uint32_t w = __ldg(reinterpret_cast<const uint32_t*>(a.codes[which] + at * (kD / 2) + (c0 >> 1)));
+    const uint32_t w = __ldg(reinterpret_cast<const uint32_t*>(a.codes[which] + at * (kD / 2) + ((c0 >> 1) & ~3))) >>
+                       (4 * (c0 & 4));
     const float s = __ldg(a.scale[which] + at);
-    float y[8];
+    float y[kCh];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) y[i] = static_cast<float>(static_cast<int>(w << (28 - 4 * i)) >> 28) * s;
+    for (int i = 0; i < kCh; ++i) y[i] = static_cast<float>(static_cast<int>(w << (28 - 4 * i)) >> 28) * s;
     const size_t o = ((static_cast<size_t>(blockIdx.z) * a.Hk + h) * a.T + t) * kD + c0;
-    if constexpr (kBf16) {
-      uint32_t p[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const __nv_bfloat162 h2 = __floats2bfloat162_rn(y[2 * i], y[2 * i + 1]);
-        p[i] = *reinterpret_cast<const uint32_t*>(&h2);
-      }
-      *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.y[which]) + o) = make_uint4(p[0], p[1], p[2], p[3]);
-    } else {
-      float4* dst = reinterpret_cast<float4*>(static_cast<float*>(a.y[which]) + o);
-      dst[0] = make_float4(y[0], y[1], y[2], y[3]);
-      dst[1] = make_float4(y[4], y[5], y[6], y[7]);
-    }
+    if constexpr (kBf16)
+      *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.y[which]) + o) =
+          make_uint4(pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3]), pack_bf16(y[4], y[5]), pack_bf16(y[6], y[7]));
+    else
+      *reinterpret_cast<float4*>(static_cast<float*>(a.y[which]) + o) = make_float4(y[0], y[1], y[2], y[3]);
   }
 }
 
@@ -600,16 +607,16 @@ __global__ void __launch_bounds__(128) kv4_join_kernel(Kv4Parts parts, int nspli
 int log2_of(int x) { return __builtin_ctz(static_cast<unsigned>(x)); }
 
 CacheArgs cache_args(const ra_kv4_cache& c, int B, int T, const int32_t* table, int max_pages, const int32_t* start,
-                     const int32_t* count, dim3* grid) {
+                     const int32_t* count, int lanes, dim3* grid) {
   CacheArgs a{};
   a.codes[0] = c.k4; a.codes[1] = c.v4;
   a.scale[0] = c.sk; a.scale[1] = c.sv;
   a.table = table; a.start = start; a.count = count;
   a.num_pages = c.num_pages; a.page_log2 = log2_of(c.page_size); a.max_pages = max_pages;
   a.Hk = c.Hk; a.T = T;
-  const int tok = (kThreads / 32) * (256 / c.D);
+  const int tok = kThreads / lanes;  // tokens per CTA
   const int tiles = (T + tok - 1) / tok;
-  int group = 8;  // heads per CTA: as many as leave eight CTAs per SM, at most eight
+  int group = 64;  // heads per CTA: as many as leave eight CTAs per SM, at most 64
   while (group > 1 && static_cast<long long>(tiles) * B * 2 * ((c.Hk + group - 1) / group) < 8LL * kNumSMs) group >>= 1;
   a.group = group;
   a.groups = (c.Hk + group - 1) / group;
@@ -632,7 +639,7 @@ cudaError_t launch_kv4_append(const ra_kv4_cache& c, int dtype, int B, int T, co
                               const void* v, const ra_strides& vs, const int32_t* table, int max_pages,
                               const int32_t* start, const int32_t* n_new, cudaStream_t st) {
   dim3 grid;
-  CacheArgs a = cache_args(c, B, T, table, max_pages, start, n_new, &grid);
+  CacheArgs a = cache_args(c, B, T, table, max_pages, start, n_new, c.D / 8, &grid);
   a.x[0] = k; a.x[1] = v;
   a.st[0] = ks; a.st[1] = vs;
   if (dtype == RA_DT_BF16) {
@@ -648,7 +655,7 @@ cudaError_t launch_kv4_append(const ra_kv4_cache& c, int dtype, int B, int T, co
 cudaError_t launch_kv4_read(const ra_kv4_cache& c, int dtype, int B, int T, const int32_t* table, int max_pages,
                             const int32_t* start, const int32_t* n, void* k, void* v, cudaStream_t st) {
   dim3 grid;
-  CacheArgs a = cache_args(c, B, T, table, max_pages, start, n, &grid);
+  CacheArgs a = cache_args(c, B, T, table, max_pages, start, n, dtype == RA_DT_BF16 ? c.D / 8 : c.D / 4, &grid);
   a.y[0] = k; a.y[1] = v;
   if (dtype == RA_DT_BF16) {
     if (c.D == 64) kv4_read_kernel<true, 64><<<grid, kThreads, 0, st>>>(a);

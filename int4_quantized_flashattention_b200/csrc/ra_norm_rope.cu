@@ -52,7 +52,8 @@ __device__ __forceinline__ float group_sum(float v, int lpt) {
 
 // kRot: the rotation, or -1 for the norm alone.
 template <bool kBf16, int kD, int kRot, bool kLayer>
-__global__ void __launch_bounds__(kThreads) norm_rope_kernel(const NormArgs a) {
+__global__ void __launch_bounds__(kThreads, 3) norm_rope_kernel(const NormArgs a) {
+  constexpr int kAhead = kBf16 ? 4 : 2;  // heads whose loads travel while as many are worked on
   constexpr int kLanes = kD / 8, kTok = 32 / kLanes;  // lanes per row, tokens per warp
   __shared__ float rows[kRot == RA_ROT_HALF ? kThreads / 32 : 1][kTok][kD];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -63,6 +64,11 @@ __global__ void __launch_bounds__(kThreads) norm_rope_kernel(const NormArgs a) {
   const int n = (blockIdx.x * (kThreads / 32) + warp) * kTok + tok;
   const bool in_range = n < a.N;
   const int nc = in_range ? n : a.N - 1;  // lanes past the end work on the last row and do not store
+  const size_t src = blockIdx.z * a.st[which].b + nc * a.st[which].n + c0;
+  Raw8<kBf16> next[kAhead];
+#pragma unroll
+  for (int i = 0; i < kAhead; ++i)
+    if (h0 + i < h1) load_raw8<kBf16>(a.x[which], src + (h0 + i) * a.st[which].h, next[i]);
   RopePlan rp;
   float2 cf[4];
   if constexpr (kRot >= 0) {
@@ -78,37 +84,44 @@ __global__ void __launch_bounds__(kThreads) norm_rope_kernel(const NormArgs a) {
     w[i] = a.weight[which] ? __ldg(a.weight[which] + c0 + i) : 1.0f;
     b[i] = a.bias[which] ? __ldg(a.bias[which] + c0 + i) : 0.0f;
   }
-  const size_t src = blockIdx.z * a.st[which].b + nc * a.st[which].n + c0;
   const size_t hn = static_cast<size_t>(a.N) * kD;
   __nv_bfloat16* dst = a.out[which] + blockIdx.z * hn * a.heads[which] + static_cast<size_t>(nc) * kD + c0;
-#pragma unroll 4
-  for (int h = h0; h < h1; ++h) {
-    Raw8<kBf16> raw;
-    load_raw8<kBf16>(a.x[which], src + h * a.st[which].h, raw);
-    float x[8];
-    unpack8<kBf16>(raw, x);
-    if constexpr (kLayer) {
-      float s = 0.0f;
+  for (int hb = h0; hb < h1; hb += kAhead) {
+    Raw8<kBf16> cur[kAhead];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) s += x[i];
-      const float mu = group_sum(s, kLanes) * (1.0f / kD);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) x[i] -= mu;
+    for (int i = 0; i < kAhead; ++i) {
+      cur[i] = next[i];
+      if (hb + kAhead + i < h1) load_raw8<kBf16>(a.x[which], src + (hb + kAhead + i) * a.st[which].h, next[i]);
     }
-    float ss = 0.0f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) ss = fmaf(x[i], x[i], ss);
-    const float r = rsqrtf(fmaf(group_sum(ss, kLanes), 1.0f / kD, a.eps));
+    for (int u = 0; u < kAhead; ++u) {
+      const int h = hb + u;
+      if (h >= h1) break;
+      float x[8];
+      unpack8<kBf16>(cur[u], x);
+      if constexpr (kLayer) {
+        float s = 0.0f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = fmaf(x[i] * r, w[i], b[i]);
-    if constexpr (kRot >= 0) rope_apply8(a.s, rp, kRot, cf, c0, x, rows[kRot == RA_ROT_HALF ? warp : 0][tok]);
-    uint32_t o[4];
+        for (int i = 0; i < 8; ++i) s += x[i];
+        const float mu = group_sum(s, kLanes) * (1.0f / kD);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const __nv_bfloat162 h2 = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
-      o[i] = *reinterpret_cast<const uint32_t*>(&h2);
+        for (int i = 0; i < 8; ++i) x[i] -= mu;
+      }
+      float ss = 0.0f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) ss = fmaf(x[i], x[i], ss);
+      const float r = rsqrtf(fmaf(group_sum(ss, kLanes), 1.0f / kD, a.eps));
+#pragma unroll
+      for (int i = 0; i < 8; ++i) x[i] = fmaf(x[i] * r, w[i], b[i]);
+      if constexpr (kRot >= 0) rope_apply8(a.s, rp, kRot, cf, c0, x, rows[kRot == RA_ROT_HALF ? warp : 0][tok]);
+      uint32_t o[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const __nv_bfloat162 h2 = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
+        o[i] = *reinterpret_cast<const uint32_t*>(&h2);
+      }
+      if (in_range) *reinterpret_cast<uint4*>(dst + h * hn) = make_uint4(o[0], o[1], o[2], o[3]);
     }
-    if (in_range) *reinterpret_cast<uint4*>(dst + h * hn) = make_uint4(o[0], o[1], o[2], o[3]);
   }
 }
 
@@ -151,8 +164,10 @@ cudaError_t launch_norm_rope(const ra_problem& p, const NormRopeCall& c, cudaStr
   a.s = seg_info(p);
   const int tok = (kThreads / 32) * (256 / p.D);  // tokens per CTA
   const int tiles = (p.N + tok - 1) / tok;
-  // Heads per CTA: as many as leave eight CTAs per SM, at most eight.
-  int group = 8;
+  // Heads per CTA: as many as leave eight CTAs per SM, at most 64.  A CTA begins with
+  // a chain of loads (positions, table), which eight heads did not pay for: 285 us
+  // against 228 for 32760 tokens x 80 heads.
+  int group = 64;
   while (group > 1 && static_cast<long long>(tiles) * p.B * ((heads + group - 1) / group) < 8LL * kNumSMs) group >>= 1;
   a.group = group;
   a.groups_q = (a.heads[0] + group - 1) / group;
