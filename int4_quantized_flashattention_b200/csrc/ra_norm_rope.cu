@@ -53,9 +53,9 @@ __device__ __forceinline__ float group_sum(float v, int lpt) {
 // kRot: the rotation, or -1 for the norm alone.
 template <bool kBf16, int kD, int kRot, bool kLayer>
 __global__ void __launch_bounds__(kThreads, 3) norm_rope_kernel(const NormArgs a) {
-  constexpr int kAhead = kBf16 ? 4 : 2;  // heads whose loads travel while as many are worked on
   constexpr int kLanes = kD / 8, kTok = 32 / kLanes;  // lanes per row, tokens per warp
-  __shared__ float rows[kRot == RA_ROT_HALF ? kThreads / 32 : 1][kTok][kD];
+  constexpr int kAhead = kBf16 ? 4 : 2;  // heads whose loads travel while as many are worked on
+  __shared__ float rows[kRot == RA_ROT_HALF ? kThreads / 32 : 1][kRot == RA_ROT_HALF ? kAhead : 1][kTok][kD];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int tok = lane / kLanes, c0 = (lane % kLanes) * 8;
   const int which = static_cast<int>(blockIdx.y) >= a.groups_q ? 1 : 0;
@@ -65,7 +65,7 @@ __global__ void __launch_bounds__(kThreads, 3) norm_rope_kernel(const NormArgs a
   const bool in_range = n < a.N;
   const int nc = in_range ? n : a.N - 1;  // lanes past the end work on the last row and do not store
   const size_t src = blockIdx.z * a.st[which].b + nc * a.st[which].n + c0;
-  Raw8<kBf16> next[kAhead];
+  Raw8<kBf16> next[kAhead] = {};
 #pragma unroll
   for (int i = 0; i < kAhead; ++i)
     if (h0 + i < h1) load_raw8<kBf16>(a.x[which], src + (h0 + i) * a.st[which].h, next[i]);
@@ -94,9 +94,8 @@ __global__ void __launch_bounds__(kThreads, 3) norm_rope_kernel(const NormArgs a
       if (hb + kAhead + i < h1) load_raw8<kBf16>(a.x[which], src + (hb + kAhead + i) * a.st[which].h, next[i]);
     }
 #pragma unroll
-    for (int u = 0; u < kAhead; ++u) {
+    for (int u = 0; u < kAhead; ++u) {  // heads past the last one are worked on but not stored
       const int h = hb + u;
-      if (h >= h1) break;
       float x[8];
       unpack8<kBf16>(cur[u], x);
       if constexpr (kLayer) {
@@ -113,14 +112,14 @@ __global__ void __launch_bounds__(kThreads, 3) norm_rope_kernel(const NormArgs a
       const float r = rsqrtf(fmaf(group_sum(ss, kLanes), 1.0f / kD, a.eps));
 #pragma unroll
       for (int i = 0; i < 8; ++i) x[i] = fmaf(x[i] * r, w[i], b[i]);
-      if constexpr (kRot >= 0) rope_apply8(a.s, rp, kRot, cf, c0, x, rows[kRot == RA_ROT_HALF ? warp : 0][tok]);
+      if constexpr (kRot >= 0) rope_apply8(a.s, rp, kRot, cf, c0, x, rows[kRot == RA_ROT_HALF ? warp : 0][kRot == RA_ROT_HALF ? u : 0][tok]);
       uint32_t o[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const __nv_bfloat162 h2 = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
         o[i] = *reinterpret_cast<const uint32_t*>(&h2);
       }
-      if (in_range) *reinterpret_cast<uint4*>(dst + h * hn) = make_uint4(o[0], o[1], o[2], o[3]);
+      if (in_range && h < h1) *reinterpret_cast<uint4*>(dst + h * hn) = make_uint4(o[0], o[1], o[2], o[3]);
     }
   }
 }
@@ -143,11 +142,29 @@ cudaError_t launch_rot(const NormArgs& a, int rot, bool layer, dim3 grid, cudaSt
   }
 }
 
+// Heads of two tensors that a CTA of a row-wise kernel walks over, for `tiles`
+// token tiles and `per_sm` CTAs at once on an SM: the waves of CTAs times their
+// length, in heads, a CTA's start counted as four of them.
+int heads_per_cta(long long tiles, const int* heads, int per_sm) {
+  int best = 1;
+  long long best_cost = -1;
+  for (int g = 1; g <= 64; ++g) {
+    const long long ctas = tiles * ((heads[0] + g - 1) / g + (heads[1] + g - 1) / g);
+    const long long slots = static_cast<long long>(per_sm) * kNumSMs;
+    // a grid of many waves ends as its last CTAs do: half a wave of waste at most
+    const long long cost = ctas <= 4 * slots ? (ctas + slots - 1) / slots * (g + 4) * 16 : ctas * (g + 4) * 16 / slots + (g + 4) * 8;
+    if (best_cost < 0 || cost < best_cost) {
+      best = g;
+      best_cost = cost;
+    }
+  }
+  return best;
+}
+
 }  // namespace
 
 cudaError_t launch_norm_rope(const ra_problem& p, const NormRopeCall& c, cudaStream_t st) {
   NormArgs a{};
-  int heads = 0;
   for (int i = 0; i < 2; ++i) {
     a.x[i] = c.x[i];
     a.st[i] = c.st[i];
@@ -155,7 +172,6 @@ cudaError_t launch_norm_rope(const ra_problem& p, const NormRopeCall& c, cudaStr
     a.bias[i] = c.bias[i];
     a.out[i] = static_cast<__nv_bfloat16*>(c.out[i]);
     a.heads[i] = c.x[i] ? c.heads[i] : 0;
-    heads += a.heads[i];
   }
   a.N = p.N;
   a.eps = c.eps;
@@ -164,11 +180,9 @@ cudaError_t launch_norm_rope(const ra_problem& p, const NormRopeCall& c, cudaStr
   a.s = seg_info(p);
   const int tok = (kThreads / 32) * (256 / p.D);  // tokens per CTA
   const int tiles = (p.N + tok - 1) / tok;
-  // Heads per CTA: as many as leave eight CTAs per SM, at most 64.  A CTA begins with
-  // a chain of loads (positions, table), which eight heads did not pay for: 285 us
-  // against 228 for 32760 tokens x 80 heads.
-  int group = 64;
-  while (group > 1 && static_cast<long long>(tiles) * p.B * ((heads + group - 1) / group) < 8LL * kNumSMs) group >>= 1;
+  // A CTA begins with a chain of loads (positions, table), which eight heads do not
+  // pay for (32760 tokens x 80 heads: 285 us against 211).
+  const int group = heads_per_cta(static_cast<long long>(tiles) * p.B, a.heads, 3);
   a.group = group;
   a.groups_q = (a.heads[0] + group - 1) / group;
   const dim3 grid(tiles, a.groups_q + (a.heads[1] + group - 1) / group, p.B);
