@@ -66,8 +66,9 @@ struct CfgT {
   static constexpr int oK = oQ + kTiles * kQBytes;
   static constexpr int oV = oK + kStages * kKVBytes;
   static constexpr int oScale = oV + kStages * kKVBytes;      // [sk | sv][stage][key], cache only
-  static constexpr int oStage = oScale + (KV4 ? 2 * kStages * kKeys * 4 : 0);  // [softmax warp][row][64 bytes]
-  static constexpr int oBar = oStage + 8 * 32 * 64;
+  static constexpr int oStage = oScale + (KV4 ? 2 * kStages * kKeys * 4 : 0);  // [softmax warp][row][kPiece]
+  static constexpr int kPiece = KV4 ? 64 : 128;        // bytes of a row that leave at a time
+  static constexpr int oBar = oStage + 8 * 32 * kPiece;
   static constexpr int kNumBars = 2 + 2 + 5 * kStages + 4 + 4 + 4 + 2 + 8;
   static constexpr int oMisc = oBar + kNumBars * 8;
   static constexpr int kSmem = oMisc + 16 + 1024;
@@ -563,51 +564,56 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
       const size_t at = bh * a.R + r;
       const bool split = KV4 && a.nsplit > 1;
       const size_t prow = static_cast<size_t>(it.split) * (a.nitems / (a.npairs * a.nsplit)) * a.R + at;
-      // Rows leave through shared memory, 64 bytes of each at a time: four lanes
-      // write a row's piece together (a thread writing its own row touched 32
-      // lines per store, 1900 cycles a block at 4 blocks per item).
+      // Rows leave through shared memory, kPiece bytes of each at a time, neighbouring
+      // lanes a piece together: a thread writing its own row touched 32 lines per
+      // store, 7800 cycles an item at 512 keys against 1900.
       const uint32_t live = __ballot_sync(0xFFFFFFFFu, row_live);
-      uint8_t* const stage = smem + C::oStage + (warp - C::kFirstSoftmax) * (32 * 64);
-      const int rbase = it.row0 + tt * kRows + quad * 32;
-      auto put = [&](const uint32_t* w, uint8_t* base, int64_t row_bytes) {  // 16 words of each row
+      constexpr int kChunks = C::kPiece / 16, kAtOnce = 32 / kChunks;  // chunks of a piece, rows per store
+      auto place = [&](int row, int ch) {  // a row's chunks lie in other banks than its neighbours'
+        return smem + C::oStage + ((warp - C::kFirstSoftmax) * 32 + row) * C::kPiece +
+               ((ch ^ (row * C::kPiece >> 7 & (kChunks - 1))) << 4);
+      };
+      const int64_t rbase = it.row0 + tt * kRows + quad * 32;
+      auto put = [&](const uint32_t* w, void* dst, int64_t row_bytes) {  // kPiece bytes of each row
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          *reinterpret_cast<uint4*>(stage + lane * 64 + ((i ^ ((lane >> 1) & 3)) << 4)) =
-              make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+        for (int i = 0; i < kChunks; ++i)
+          *reinterpret_cast<uint4*>(place(lane, i)) = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
         __syncwarp();
+        const int ch = lane % kChunks;
+        uint8_t* p = static_cast<uint8_t*>(dst) + (lane / kChunks) * row_bytes + ch * 16;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int row = 8 * i + (lane >> 2), ch = lane & 3;
-          const uint4 v = *reinterpret_cast<const uint4*>(stage + row * 64 + ((ch ^ ((row >> 1) & 3)) << 4));
-          if ((live >> row) & 1u) *reinterpret_cast<uint4*>(base + row * row_bytes + ch * 16) = v;
+        for (int row = lane / kChunks, i = 0; i < kChunks; ++i, row += kAtOnce, p += kAtOnce * row_bytes) {
+          const uint4 v = *reinterpret_cast<const uint4*>(place(row, ch));
+          if ((live >> row) & 1u) *reinterpret_cast<uint4*>(p) = v;
         }
         __syncwarp();
       };
+      constexpr int kPass = C::kPiece / 2;  // channels
 #pragma unroll
-      for (int c = 0; c < D; c += 32) {
-        uint32_t o[32];
+      for (int c = 0; c < D; c += kPass) {
+        uint32_t o[kPass];
         if (it.nb > 0) {
-          tmem_ld_row<32>(tO + c, o);
+          tmem_ld_row<kPass>(tO + c, o);
         } else {
 #pragma unroll
-          for (int i = 0; i < 32; ++i) o[i] = 0u;
+          for (int i = 0; i < kPass; ++i) o[i] = 0u;
         }
-        float x[32];
+        float x[kPass];
 #pragma unroll
-        for (int i = 0; i < 32; ++i) {
+        for (int i = 0; i < kPass; ++i) {
           // cache: column 2i + e of eight holds channel i + 4e
           const int from = KV4 ? (i & ~7) + 2 * (i & 3) + ((i >> 2) & 1) : i;
           x[i] = some ? __uint_as_float(o[from]) * inv : 0.0f;
         }
         if (split) {
-          uint8_t* const dst = reinterpret_cast<uint8_t*>(a.parts.o + (prow - lane) * D + c);
+          float* const dst = a.parts.o + (prow - lane) * D + c;
           put(reinterpret_cast<const uint32_t*>(x), dst, D * 4);
-          put(reinterpret_cast<const uint32_t*>(x + 16), dst + 64, D * 4);
+          put(reinterpret_cast<const uint32_t*>(x + kPass / 2), dst + kPass / 2, D * 4);
         } else {
-          uint32_t w[16];
+          uint32_t w[kPass / 2];
 #pragma unroll
-          for (int i = 0; i < 16; ++i) w[i] = pack_bf16(x[2 * i], x[2 * i + 1]);
-          put(w, reinterpret_cast<uint8_t*>(a.out + it.b * a.os.b + it.h * a.os.h + rbase * a.os.n + c), a.os.n * 2);
+          for (int i = 0; i < kPass / 2; ++i) w[i] = pack_bf16(x[2 * i], x[2 * i + 1]);
+          put(w, a.out + it.b * a.os.b + it.h * a.os.h + rbase * a.os.n + c, a.os.n * 2);
         }
       }
       tc_fence_before();
