@@ -7,31 +7,18 @@
 // per tile, so the tensor cores work on one block while the softmax is at the
 // other: with 128-key blocks and one buffer a tile's products and its softmax
 // took turns (890 TFLOP/s at 8192 x 8192, D = 128, softmax warps idle half of
-// the time; 1157 now).  The two tiles' warps of a quarter share an SM partition and
-// its exponentials (8 cycles a warp instruction, 512 a block); left alone they
-// fell into step, both at the exponentials or both at none.  They take turns
-// (turn_of): 732 cycles a block for a warp's exponentials instead of 1150.
-// What bounds it, at D = 128: shared memory, 1280 of 1750 cycles a block (S with
-// N = 64 reads Q again for every block, 48 cycles an MMA against 32 of
-// arithmetic; P V 64), and the hops between the MMAs and the softmax; at D = 64
-// the exponentials.  Measured and left out: exponentials of every 4th to 12th
-// pair by a polynomial (2 to 12 % slower), P beside S so that S(g + 1) need not
-// wait for P V(g - 1) (4 % slower), 16 softmax warps (6 % slower, 20 % for the
-// cache), four warps of their own for the output (6 % slower at 8192 keys, 3 %
-// faster at 512, 13 % slower at 128).
-//   warp 0      TMA producer: Q, and (cross) K and V, 64-channel boxes with the
-//               128-byte swizzle
-//   warps 1, 2  MMA issuers of tiles 0 and 1: S = Q K^T into TMEM (tcgen05
-//               kind::f16, M = 128, N = 64), then O += P V with P read from TMEM
-//   warp 3      (cross) clears value rows behind the last key, which may hold
-//               anything, before the MMA reads them: 0 * NaN is not 0
-//   warps 4-7   (cache) unpack codes into bf16 K and V tiles (exact); a thread
-//               per key, the next block's codes in flight in its registers
-//   then 4 + 4  softmax warps, one row per thread: no exchange between threads.
-// P overwrites the S columns it came from.  The reference maximum moves only when a score passes it by 2^8
-// (kLazy): rescaling O in TMEM is rare, and P stays below 2^8, which bf16
-// holds as well as 1.  The scales of the cache multiply the scores (keys) and
-// P before its rounding (values) in fp32.
+// the time; 1290 now).  What bounds it at D = 128: shared memory, 1280 of 1570 cycles
+// a block (S with N = 64 reads Q again for every block, 48 cycles an MMA against 32 of
+// arithmetic; P V 64 an MMA), and the exponentials, 1024 (8 cycles a warp
+// instruction, 16384 of them a block and partition); at D = 64 the exponentials; the
+// cache's kernel besides what the unpacking warps take of the issue slots and of shared
+// memory.  Issuing an MMA costs 16 cycles only from a thread that the compiler knows to
+// be alone (elect_one); under a test of the lane it cost 56 to 100, and the kernel was
+// bound by it (1157 TFLOP/s).  Measured and left out, some of it under that bound:
+// exponentials of every fourth pair by a polynomial on the FMA pipe (3 % slower at
+// 8192 keys, 1 % faster at 512), P beside S so that S(g + 1) need not wait for
+// P V(g - 1) (4 % slower), 16 softmax warps (6 % slower, 20 % for the cache), four warps
+// of their own for the output (6 % slower at 8192 keys, 3 % faster at 512).
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <cuda_bf16.h>
@@ -52,7 +39,11 @@ __device__ uint32_t g_tiles_status = 0;
 constexpr int kRows = 128;   // query rows per tile = MMA M
 constexpr int kTiles = 2;    // query tiles per CTA
 constexpr int kKeys = 64;    // keys per block = MMA N of S
-constexpr float kLazy = 8.0f;
+// The reference maximum moves when a score passes it by kLazy (powers of two).
+template <bool KV4> constexpr float kLazy = KV4 ? 4.0f : 8.0f;
+constexpr float kPUp = 11.0f;  // cache: P goes to f16 times 2^kPUp, at most 2^15
+constexpr int kVUp = 12;       // and the values times 2^kVUp, at most 7 * 2^12: a scale keeps its bits down to
+                               // 2^-26 of the largest of its 32 keys
 
 template <int D, bool KV4>
 struct CfgT {
@@ -69,13 +60,17 @@ struct CfgT {
   static constexpr int oStage = oScale + (KV4 ? 2 * kStages * kKeys * 4 : 0);  // [softmax warp][row][kPiece]
   static constexpr int kPiece = KV4 ? 64 : 128;        // bytes of a row that leave at a time
   static constexpr int oBar = oStage + 8 * 32 * kPiece;
-  static constexpr int kNumBars = 2 + 2 + 5 * kStages + 4 + 4 + 4 + 2 + 8;
+  static constexpr int kNumBars = 2 + 2 + 5 * kStages + 4 + 4 + 4 + 2;
   static constexpr int oMisc = oBar + kNumBars * 8;
   static constexpr int kSmem = oMisc + 16 + 1024;
-  static constexpr int kFirstSoftmax = KV4 ? 8 : 4;
+  // Unpacking warps: at D = 128 four for the keys and four for the values (1380 us
+  // against 1453 at 1560 x 32760 x 40 heads), at D = 64, where the softmax is the
+  // slower side, four for both (1199 us against 1426).
+  static constexpr bool kTwoUnpack = KV4 && D == 128;
+  static constexpr int kFirstSoftmax = KV4 ? (kTwoUnpack ? 12 : 8) : 4;
   static constexpr int kThreads = (kFirstSoftmax + 8) * 32;
   static constexpr uint32_t kIdescQK = instr_desc(kCfmtF32, 1, 1, 0, 0, kRows, kKeys);
-  static constexpr uint32_t kIdescPV = instr_desc(kCfmtF32, 1, 1, 0, 1, kRows, D);
+  static constexpr uint32_t kIdescPV = instr_desc(kCfmtF32, KV4 ? 0 : 1, KV4 ? 0 : 1, 0, 1, kRows, D);
   static_assert(kSmem <= 232448, "shared memory");
 };
 
@@ -184,7 +179,6 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
   uint64_t* const s_full = b; b += 4;              // [tile][buffer]
   uint64_t* const p_full = b; b += 4;
   uint64_t* const pv_done = b; b += 4;
-  uint64_t* const turn_of = b; b += 8;             // [tile][quarter]: whose exponentials run
   uint64_t* const drain = b;
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + C::oMisc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::oMisc + 4);
@@ -199,7 +193,6 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
       mbar_init(k_full + i, KV4 ? 4 : 1); mbar_init(k_empty + i, KV4 ? 2 + 8 : 2);
       mbar_init(v_full + i, 1); mbar_init(v_ready + i, KV4 ? 4 : 1); mbar_init(v_empty + i, KV4 ? 2 + 8 : 2);
     }
-    for (int i = 0; i < 8; ++i) mbar_init(turn_of + i, 1);
     *abort_flag = 0;
     fence_barrier_init();
   }
@@ -215,13 +208,15 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
   __syncthreads();
   tc_fence_after();
   const uint32_t tbase = *tmem_holder;
-  float* const scales = reinterpret_cast<float*>(smem + C::oScale);
+  float* const scales = reinterpret_cast<float*>(smem + C::oScale);  // cache: of the keys
+  float* const v_exp = scales + C::kStages * kKeys;                   // cache: exponents of the values' scales
   uint32_t bad = 0;
   bool ok = true;
   if (warp < 4) {
     if constexpr (KV4) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
     else asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
-    if (warp == 0 && lane == 0) {
+    const bool one = elect_one();  // the thread that issues; ptxas knows it to be alone, a test of the lane it does not
+    if (warp == 0 && one) {
       // ------------------------------------------------------------ TMA producer
       uint32_t g = 0, li = 0;
       for (int item = blockIdx.x; item < a.nitems && ok; item += gridDim.x) {
@@ -269,13 +264,13 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
       if (li > 0)
         for (int tt = 0; tt < kTiles; ++tt)
           while (!mbar_try_wait(q_full + tt, (li - 1) & 1) && ++n < kSpinLimit) {}
-    } else if ((warp == 1 || warp == 2) && lane == 0) {
+    } else if ((warp == 1 || warp == 2) && one) {
       // ------------------------------------------------------------ MMA issuers
       // Per tile: P V(g), then S(g + 2) into the buffer whose P it has read (after
       // it has completed: products into different accumulators are not ordered).
       const int tt = warp - 1;
-      const uint32_t sQ = smem_u32(smem + C::oQ) + tt * C::kQBytes;
-      const uint32_t sK = smem_u32(smem + C::oK), sV = smem_u32(smem + C::oV);
+      const uint32_t dQ = desc_lo(smem_u32(smem + C::oQ) + tt * C::kQBytes, 16);
+      const uint32_t dK = desc_lo(smem_u32(smem + C::oK), 16), dV = desc_lo(smem_u32(smem + C::oV), C::kHalf);
       const uint32_t tS0 = tbase + tt * 128, tO = tbase + 256 + tt * 128;
       uint32_t g0 = 0, li = 0;
       auto scores = [&](uint32_t g, bool last) -> bool {
@@ -284,13 +279,11 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
         if (!wait_t(k_full + s, (g / C::kStages) & 1, abort_flag)) return false;
         if (g >= 2 && !wait_t(pv_done + tt * 2 + buf, ((g - 2) >> 1) & 1, abort_flag)) return false;
         tc_fence_after();
+        const uint32_t k = dK + s * (C::kKVBytes >> 4);
 #pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) {
-          const uint32_t off = (kk & 3) * 32;
-          mma_f16_ss(tS0 + buf * 64, smem_desc(sQ + (kk >> 2) * C::kQHalf + off, 16, 1024, kSwizzle128B),
-                     smem_desc(sK + s * C::kKVBytes + (kk >> 2) * C::kHalf + off, 16, 1024, kSwizzle128B),
-                     C::kIdescQK, kk > 0 ? 1u : 0u);
-        }
+        for (int kk = 0; kk < D / 16; ++kk)
+          mma_ss<C::kIdescQK>(tS0 + buf * 64, dQ + (kk >> 2) * (C::kQHalf >> 4) + (kk & 3) * 2,
+                              k + (kk >> 2) * (C::kHalf >> 4) + (kk & 3) * 2, kk > 0);
         mma_commit(s_full + tt * 2 + buf);
         mma_commit(k_empty + s);
         if (last) mma_commit(q_free + tt);
@@ -308,11 +301,10 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
           if (!(ok = wait_t(v_ready + s, (g / C::kStages) & 1, abort_flag))) break;
           if (!(ok = wait_t(p_full + tt * 2 + buf, (g >> 1) & 1, abort_flag))) break;
           tc_fence_after();
+          const uint32_t v = dV + s * (C::kKVBytes >> 4);
 #pragma unroll
           for (int kk = 0; kk < kKeys / 16; ++kk)
-            mma_f16_ts(tO, tS0 + buf * 64 + kk * 8,
-                       smem_desc(sV + s * C::kKVBytes + kk * 16 * 128, C::kHalf, 1024, kSwizzle128B), C::kIdescPV,
-                       t > 0 || kk > 0 ? 1u : 0u);
+            mma_ts<C::kIdescPV>(tO, tS0 + buf * 64 + kk * 8, v + kk * (16 * 128 >> 4), kk > 0 || t > 0);
           mma_commit(pv_done + tt * 2 + buf);
           mma_commit(v_empty + s);
           if (t + 2 < it.nb) ok = scores(g + 2, t + 2 == it.nb - 1);
@@ -345,9 +337,10 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
         }
       }
     }
-  } else if (KV4 && warp < 8) {
+  } else if (KV4 && warp < C::kFirstSoftmax) {
     // -------------------------------------------------------------- unpacking warps
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    if constexpr (C::kTwoUnpack) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+    else asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
     if constexpr (KV4) {
       constexpr int kQ = D / 64;  // 16-byte pieces of a code row per thread: two threads per key
       const int row = threadIdx.x & 63, part = (threadIdx.x >> 6) & 1;
@@ -374,61 +367,101 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
           s = 0.0f;
         }
       };
+      // Keys of block g: bf16, eight channels in their order.
+      auto put_keys = [&](const uint4* code, float scale, uint32_t g) -> bool {
+        const int s = g % C::kStages;
+        if (!wait_warp(k_empty + s, ((g / C::kStages) & 1) ^ 1, abort_flag)) return false;
+        uint8_t* const kt = smem + C::oK + s * C::kKVBytes + row * 128;
+#pragma unroll
+        for (int i = 0; i < kQ; ++i) {
+          const uint32_t w[4] = {code[i].x, code[i].y, code[i].z, code[i].w};
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            const uint32_t p0 = codes_bf16(w[c]), p1 = codes_bf16(w[c] >> 4);
+            const uint32_t p2 = codes_bf16(w[c] >> 8), p3 = codes_bf16(w[c] >> 12);
+            const uint4 o = make_uint4(__byte_perm(p0, p1, 0x5410), __byte_perm(p2, p3, 0x5410),
+                                       __byte_perm(p0, p1, 0x7632), __byte_perm(p2, p3, 0x7632));
+            const int ch = (part * kQ + i) * 4 + c;
+            *reinterpret_cast<uint4*>(kt + (ch >> 3) * C::kHalf + (((ch & 7) ^ (row & 7)) << 4)) = o;
+          }
+        }
+        if (part == 0) scales[s * kKeys + row] = scale * a.scale_log2;
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(k_full + s);
+        return true;
+      };
+      // Values of block g: f16, with their scale, relative (2^kVUp) to the power of two not below
+      // the largest scale of these 32 keys (whose exponent the softmax puts into P);
+      // channels 0 4 1 5 2 6 3 7 of eight, which the output puts right.
+      auto put_values = [&](const uint4* code, float scale, uint32_t g) -> bool {
+        const int s = g % C::kStages;
+        float vm = scale;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) vm = fmaxf(vm, __shfl_xor_sync(0xFFFFFFFFu, vm, o));
+        const uint32_t ve = min(max((__float_as_uint(vm) + 0x007FFFFFu) >> 23, 27u), 253u);  // 2^(ve - 127)
+        const __half2 v_scale = __float2half2_rn(scale * __uint_as_float((254u + kVUp - ve) << 23));
+        auto times = [&](uint32_t x) {
+          const __half2 r = __hmul2(*reinterpret_cast<const __half2*>(&x), v_scale);
+          return *reinterpret_cast<const uint32_t*>(&r);
+        };
+        if (!wait_warp(v_empty + s, ((g / C::kStages) & 1) ^ 1, abort_flag)) return false;
+        uint8_t* const vt = smem + C::oV + s * C::kKVBytes + row * 128;
+#pragma unroll
+        for (int i = 0; i < kQ; ++i) {
+          const uint32_t w[4] = {code[i].x, code[i].y, code[i].z, code[i].w};
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            const uint4 o = make_uint4(times(codes_f16_lo(w[c])), times(codes_f16_hi(w[c])),
+                                       times(codes_f16_lo(w[c] >> 8)), times(codes_f16_hi(w[c] >> 8)));
+            const int ch = (part * kQ + i) * 4 + c;
+            *reinterpret_cast<uint4*>(vt + (ch >> 3) * C::kHalf + (((ch & 7) ^ (row & 7)) << 4)) = o;
+          }
+        }
+        if (part == 0 && lane == 0) v_exp[s * 2 + (row >> 5)] = static_cast<float>(ve) - 127.0f;
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(v_ready + s);
+        return true;
+      };
       uint32_t g = 0;
       for (int item = blockIdx.x; item < a.nitems && ok; item += gridDim.x) {
         const Item it = get_item<KV4>(a, item, &bad);
-        long long at = place(it, 0);
-        uint4 k[kQ], v[kQ];
-        float ks, vs;
-        fetch(a.k4, a.sk, at, k, ks);
-        for (int t = 0; t < it.nb; ++t, ++g) {
-          const int s = g % C::kStages;
-          const uint32_t par = ((g / C::kStages) & 1) ^ 1;
-          fetch(a.v4, a.sv, at, v, vs);
-          if (!(ok = wait_warp(k_empty + s, par, abort_flag))) break;
-          uint8_t* const kt = smem + C::oK + s * C::kKVBytes + row * 128;
-          uint8_t* const vt = smem + C::oV + s * C::kKVBytes + row * 128;
+        // The codes of the next block travel while this one's are unpacked.
+        if constexpr (C::kTwoUnpack) {
+          const bool of_keys = warp < 8;  // warps 4-7 the keys, 8-11 the values
+          const uint8_t* const codes = of_keys ? a.k4 : a.v4;
+          const float* const from = of_keys ? a.sk : a.sv;
+          uint4 next[kQ];
+          float next_scale;
+          fetch(codes, from, place(it, 0), next, next_scale);
+          for (int t = 0; t < it.nb && ok; ++t, ++g) {
+            uint4 cur[kQ];
 #pragma unroll
-          for (int i = 0; i < kQ; ++i) {
-            const uint32_t w[4] = {k[i].x, k[i].y, k[i].z, k[i].w};
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {  // eight channels in their order
-              const uint32_t p0 = codes_bf16(w[c]), p1 = codes_bf16(w[c] >> 4);
-              const uint32_t p2 = codes_bf16(w[c] >> 8), p3 = codes_bf16(w[c] >> 12);
-              const uint4 o = make_uint4(__byte_perm(p0, p1, 0x5410), __byte_perm(p2, p3, 0x5410),
-                                         __byte_perm(p0, p1, 0x7632), __byte_perm(p2, p3, 0x7632));
-              const int ch = (part * kQ + i) * 4 + c;
-              *reinterpret_cast<uint4*>(kt + (ch >> 3) * C::kHalf + (((ch & 7) ^ (row & 7)) << 4)) = o;
-            }
+            for (int i = 0; i < kQ; ++i) cur[i] = next[i];
+            const float cur_scale = next_scale;
+            fetch(codes, from, place(it, t + 1), next, next_scale);
+            ok = of_keys ? put_keys(cur, cur_scale, g) : put_values(cur, cur_scale, g);
           }
-          if (part == 0) scales[s * kKeys + row] = ks * a.scale_log2;
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(k_full + s);
-          at = place(it, t + 1);  // the next block's codes travel under this block's values
+        } else {
+          long long at = place(it, 0);
+          uint4 k[kQ], v[kQ];
+          float ks, vs;
           fetch(a.k4, a.sk, at, k, ks);
-          if (!(ok = wait_warp(v_empty + s, par, abort_flag))) break;
-#pragma unroll
-          for (int i = 0; i < kQ; ++i) {
-            const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {  // channels 0 4 1 5 2 6 3 7 of eight; the epilogue puts them right
-              const uint4 o = make_uint4(codes_bf16(w[c]), codes_bf16(w[c] >> 4), codes_bf16(w[c] >> 8),
-                                         codes_bf16(w[c] >> 12));
-              const int ch = (part * kQ + i) * 4 + c;
-              *reinterpret_cast<uint4*>(vt + (ch >> 3) * C::kHalf + (((ch & 7) ^ (row & 7)) << 4)) = o;
-            }
+          for (int t = 0; t < it.nb; ++t, ++g) {
+            fetch(a.v4, a.sv, at, v, vs);
+            if (!(ok = put_keys(k, ks, g))) break;
+            at = place(it, t + 1);
+            fetch(a.k4, a.sk, at, k, ks);
+            if (!(ok = put_values(v, vs, g))) break;
           }
-          if (part == 0) scales[(C::kStages + s) * kKeys + row] = vs;
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(v_ready + s);
         }
       }
     }
   } else {
     // -------------------------------------------------------------- softmax, one row per thread
-    if constexpr (KV4) asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
+    if constexpr (C::kTwoUnpack) asm volatile("setmaxnreg.inc.sync.aligned.u32 152;");
+    else if constexpr (KV4) asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
     else asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
     const int tt = (warp - C::kFirstSoftmax) >> 2;
     const int quad = warp & 3;
@@ -446,14 +479,21 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
         if (a.causal) lim = max(0, it.len - it.ql + i + 1);
       }
       float m = -INFINITY, l = 0.0f;
+      float ev = -100.0f;  // cache: O holds values times 2^(kPUp + kVUp - ev)
       for (int t = 0; t < it.nb; ++t, ++g) {
         const uint32_t buf = g & 1, tS = tS0 + buf * 64;
         if (!(ok = wait_warp(s_full + tt * 2 + buf, (g >> 1) & 1, abort_flag))) break;
         tc_fence_after();
+        const int stg = g % C::kStages;
+        float e_lo = 0.0f, e_hi = 0.0f;
+        if constexpr (KV4) {  // early: their way from shared memory is long while the MMA reads it
+          if (!(ok = wait_warp(v_ready + stg, (g / C::kStages) & 1, abort_flag))) break;
+          e_lo = v_exp[stg * 2];
+          e_hi = v_exp[stg * 2 + 1];
+        }
         uint32_t raw[kKeys];
         tmem_ld_row<kKeys>(tS, raw);
         float* const s = reinterpret_cast<float*>(raw);
-        const int stg = g % C::kStages;
         if constexpr (KV4) {
           const float4* const sc = reinterpret_cast<const float4*>(scales + stg * kKeys);
 #pragma unroll
@@ -482,14 +522,26 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
         }
         float mb = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
         if constexpr (!KV4) mb *= a.scale_log2;
-        // The reference moves on the first block and when passed by kLazy.
-        const bool up = mb > m + kLazy;
-        const float f = up ? ex2_approx(m - mb) : 1.0f;
-        const bool any_up = __any_sync(0xFFFFFFFFu, up);
+        // The reference moves on the first block and when passed by kLazy, the
+        // exponent of the values when theirs is larger.
+        const bool up = mb > m + kLazy<KV4>;
+        float f = up ? ex2_approx(m - mb) : 1.0f;
         if (up) {
           m = mb;
           l *= f;
         }
+        bool turned = up;
+        if constexpr (KV4) {
+          const float et = fmaxf(e_lo, e_hi);
+          if (et > ev) {
+            f *= ex2_approx(ev - et);
+            ev = et;
+            turned = true;
+          }
+          e_lo = kPUp + fmaxf(e_lo - ev, -64.0f);  // values below 2^-64 of the largest do not count
+          e_hi = kPUp + fmaxf(e_hi - ev, -64.0f);
+        }
+        const bool any_up = __any_sync(0xFFFFFFFFu, turned);
         if (any_up && t > 0) {  // O holds the blocks before this one
           if (!(ok = wait_warp(pv_done + tt * 2 + (buf ^ 1), ((g - 1) >> 1) & 1, abort_flag))) break;
           tc_fence_after();
@@ -508,15 +560,14 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
           }
         }
         const float mr = m == -INFINITY ? 0.0f : m;
-        const float2 c2 = make_float2(a.scale_log2, a.scale_log2), m2 = make_float2(-mr, -mr);
-        float2 sum2 = make_float2(0.0f, 0.0f);
-        if (!(ok = wait_warp(turn_of + tt * 4 + quad, (g & 1) ^ (tt ^ 1), abort_flag))) break;
+        const float2 c2 = make_float2(a.scale_log2, a.scale_log2);
+        float sum = 0.0f;
 #pragma unroll
         for (int c = 0; c < kKeys; c += 32) {
+          const float shift = KV4 ? (c == 0 ? e_lo : e_hi) - mr : -mr;
+          const float2 m2 = make_float2(shift, shift);
+          float2 sum2 = make_float2(0.0f, 0.0f);
           uint32_t w[16];
-          if (KV4 && c == 0) {
-            if (!(ok = wait_warp(v_ready + stg, (g / C::kStages) & 1, abort_flag))) break;
-          }
 #pragma unroll
           for (int j = 0; j < 32; j += 4) {
             float2 x = make_float2(s[c + j], s[c + j + 1]), y = make_float2(s[c + j + 2], s[c + j + 3]);
@@ -531,19 +582,13 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
             y = make_float2(ex2_approx(y.x), ex2_approx(y.y));
             sum2 = __fadd2_rn(sum2, x);
             sum2 = __fadd2_rn(sum2, y);
-            if constexpr (KV4) {
-              const float4 f4 = *reinterpret_cast<const float4*>(scales + (C::kStages + stg) * kKeys + c + j);
-              x = __fmul2_rn(x, make_float2(f4.x, f4.y));
-              y = __fmul2_rn(y, make_float2(f4.z, f4.w));
-            }
-            w[j / 2] = pack_bf16(x.x, x.y);
-            w[j / 2 + 1] = pack_bf16(y.x, y.y);
+            w[j / 2] = KV4 ? pack_f16(x.x, x.y) : pack_bf16(x.x, x.y);
+            w[j / 2 + 1] = KV4 ? pack_f16(y.x, y.y) : pack_bf16(y.x, y.y);
           }
           tmem_st_row_nw<16>(tS + c / 2, w);
+          sum += (sum2.x + sum2.y) * (KV4 ? ex2_approx(c == 0 ? -e_lo : -e_hi) : 1.0f);
         }
-        if (!ok) break;
-        if (lane == 0) mbar_arrive(turn_of + (tt ^ 1) * 4 + quad);
-        l += sum2.x + sum2.y;
+        l += sum;
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
@@ -558,7 +603,7 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
         tc_fence_after();
       }
       const bool some = m != -INFINITY;
-      const float inv = some ? 1.0f / l : 0.0f;
+      const float inv = some ? (KV4 ? ex2_approx(ev - kPUp - kVUp) : 1.0f) / l : 0.0f;
       const float lse2 = some ? m + log2f(l) : -INFINITY;
       const size_t bh = static_cast<size_t>(it.b) * a.heads + it.h;
       const size_t at = bh * a.R + r;

@@ -33,6 +33,8 @@ bool valid_dim(int D) { return D == 64 || D == 128; }
 
 bool valid_cache(const ra_kv4_cache* c) {
   if (!c || c->num_pages < 1 || c->Hk < 1 || c->Hk > kMaxGrid / 2 || !valid_dim(c->D)) return false;
+  // The kernels count the cache's rows in 32 bits (2^32 of them are more than the memory holds).
+  if (static_cast<int64_t>(c->num_pages) * c->Hk * c->page_size > (1LL << 32) - 1) return false;
   if (c->page_size != 16 && c->page_size != 32 && c->page_size != 64 && c->page_size != 128) return false;
   return aligned16(c->k4) && aligned16(c->sk) && aligned16(c->v4) && aligned16(c->sv);
 }

@@ -1,4 +1,5 @@
-// Tensor-memory accesses with one row per lane (.32x32b) and a 4D tiled TMA load.
+// Tensor-memory accesses with one row per lane (.32x32b), a 4D tiled TMA load, and
+// lean kind::f16 MMA issue.
 #pragma once
 
 #include <cstdint>
@@ -15,6 +16,38 @@ __device__ __forceinline__ void tma_load_4d(void* dst, const void* tmap, uint64_
       " [%0], [%1, {%3, %4, %5, %6}], [%2];"
       ::"r"(smem_u32(dst)), "l"(tmap), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2), "r"(c3)
       : "memory");
+}
+
+// One thread of the (converged) warp.  Code under this predicate is known to run in
+// a single thread: the operands of tcgen05.mma, which are uniform registers, then
+// move there once instead of in a loop over the active threads (measured: 16 cycles
+// to issue an MMA against 56 under a test of the lane).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred q;\n\telect.sync _|q, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, q;\n\t}" : "=r"(p));
+  return p != 0;
+}
+
+// Shared-memory descriptors as their low word (address, leading byte offset): with
+// 128-byte swizzle and a stride byte offset of 1024 the high word is a constant.
+constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (kSwizzle128B << 29);
+__device__ __forceinline__ uint32_t desc_lo(uint32_t saddr, uint32_t lbo_bytes) {
+  return (saddr >> 4) | ((lbo_bytes >> 4) << 16);
+}
+// kind::f16 with these descriptors: D[tmem] (+)= A[smem or tmem] * B[smem]
+template <uint32_t kIdesc>
+__device__ __forceinline__ void mma_ss(uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\tmov.b64 a, {%1, %4};\n\tmov.b64 b, {%2, %4};\n\t"
+      "setp.ne.b32 p, %5, 0;\n\ttcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n\t}"
+      ::"r"(d_tmem), "r"(a_lo), "r"(b_lo), "n"(kIdesc), "n"(kDescHi), "r"(accumulate) : "memory");
+}
+template <uint32_t kIdesc>
+__device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint32_t b_lo, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 b;\n\tmov.b64 b, {%2, %4};\n\t"
+      "setp.ne.b32 p, %5, 0;\n\ttcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, p;\n\t}"
+      ::"r"(d_tmem), "r"(a_tmem), "r"(b_lo), "n"(kIdesc), "n"(kDescHi), "r"(accumulate) : "memory");
 }
 
 // N consecutive 32-bit columns of each lane's TMEM row; the wait sits in the

@@ -265,6 +265,28 @@ def test_attn_sharp_and_scaled(ra, gen):
         _check_kv4(ra, c, table, lens_t, torch.ones(1, 4, Nq, 128, device="cuda", dtype=torch.bfloat16))
 
 
+@pytest.mark.parametrize("Nq", [1, 40])
+@pytest.mark.parametrize("D", [64, 128])
+def test_attn_scales_of_many_sizes(ra, gen, Nq, D):
+    """Keys and values whose rows differ by factors of up to 10^6, zero rows, and a cache that begins with tiny
+    values: the running exponent of the value scales moves many times."""
+    n = 1500
+    c, table = _make_cache(ra, gen, 2, 24, 64, 2, D)
+    k, v = _rand(gen, 2, 2, n, D), _rand(gen, 2, 2, n, D)
+    size = 10.0 ** torch.empty(2, 2, n, 1, device="cuda").uniform_(-3, 3, generator=gen)
+    size[0, 0] = 10.0 ** torch.linspace(-3, 3, n, device="cuda")[:, None]
+    v *= size
+    v[:, :, 5:40] = 0
+    k[:, :, 9:12] = 0
+    k *= 10.0 ** torch.empty(2, 2, n, 1, device="cuda").uniform_(-1.5, 0.5, generator=gen)
+    ra.kv4_append(c, k, v, table)
+    q = _rand(gen, 2, 4, Nq, D, dtype=torch.bfloat16)
+    q[:, 1] *= 1e-3
+    q[:, 2, :, :] = 0
+    _check_kv4(ra, c, table, torch.tensor([n, 33], device="cuda", dtype=torch.int32), q)
+    _check_kv4(ra, c, table, torch.tensor([n, 1001], device="cuda", dtype=torch.int32), q, causal=True)
+
+
 @pytest.mark.parametrize("causal", [False, True])
 @pytest.mark.parametrize("H,Hk,D,Nq,page,lens", [
     (1, 1, 128, 17, 16, [1]), (2, 2, 64, 33, 16, [33, 0, 127]), (4, 2, 128, 64, 64, [128, 129, 64]),
@@ -428,6 +450,53 @@ def test_streaming_block(ra, gen, n, rot):
             a = br.attention(rows[0][b], k, v, ends, D ** -0.5)[0]
             ref = br.attention(a, tk[b], tv[b], torch.full((n,), 33, device="cuda"), D ** -0.5)[0]
             assert torch.nn.functional.cosine_similarity(out[b].double().flatten(), ref.flatten(), 0) > 0.98
+
+
+def test_caches_and_tensors_past_32_bits(ra, gen):
+    """Pages and rows whose offsets pass 2^32 bytes and 2^31 elements."""
+    Hk, D, page, pages = 8, 128, 128, 72000             # 4.7 GB of codes for keys, and for values
+    c = ra.KV4Cache(*(torch.empty(pages, Hk, page, *((D // 2,) if codes else ()), device="cuda",
+                                  dtype=torch.uint8 if codes else torch.float32) for codes in (1, 0, 1, 0)))
+    table = torch.tensor([[pages - 1, 3, pages - 2]], device="cuda", dtype=torch.int32)
+    k, v = _rand(gen, 1, Hk, 300, D), _rand(gen, 1, Hk, 300, D)
+    ra.kv4_append(c, k, v, table)
+    lens = torch.tensor([300], device="cuda", dtype=torch.int32)
+    for Nq in (1, 20):
+        _check_kv4(ra, c, table, lens, _rand(gen, 1, Hk, Nq, D, dtype=torch.bfloat16))
+    del c
+    torch.cuda.empty_cache()
+    buf = torch.empty(3 * 10 ** 9, device="cuda", dtype=torch.bfloat16)
+    far = lambda n: buf.as_strided((2, 2, n, D), (2_500_000_000, 300 * D, D, 1))  # noqa: E731
+    q, out = far(200), torch.empty(2, 2, 200, D, device="cuda", dtype=torch.bfloat16)
+    q.copy_(_rand(gen, 2, 2, 200, D, dtype=torch.bfloat16))
+    _check_cross(ra, q, q, q, out=out)
+    p = ra.Problem.make(2, 2, D, SEG[D], (2, 10, 10), rot=0)
+    got, _ = ra.qk_norm_rope(p, q, None, ra.rope_table(p), _positions((2, 10, 10), 200))
+    assert torch.equal(got, ra.qk_norm_rope(p, q.contiguous(), None, ra.rope_table(p), _positions((2, 10, 10), 200))[0])
+    k2 = q.contiguous()
+    ra.attn_cross(k2, k2, k2, out=q)
+    assert torch.equal(q, ra.attn_cross(k2, k2, k2))
+
+
+def test_graph_replays_on_changed_inputs(ra, gen):
+    """A captured call with split keys (two launches, the second begun early) replays on what its tensors then hold."""
+    c, table, lens_t = _filled(ra, gen, [9000], 64, 2, 128)
+    for Nq in (1, 40):
+        q = _rand(gen, 1, 4, Nq, 128, dtype=torch.bfloat16)
+        assert ra.attn_kv4_workspace_bytes(c, 1, 4, Nq, 9000) > 0
+        ra.attn_kv4(c, q, table, lens_t)
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            out = ra.attn_kv4(c, q, table, lens_t)
+        for n in (9000, 17, 0, 5000):
+            q.copy_(_rand(gen, 1, 4, Nq, 128, dtype=torch.bfloat16))
+            lens_t.fill_(n)
+            g.replay()
+            torch.cuda.synchronize()
+            assert torch.equal(out, ra.attn_kv4(c, q, table, lens_t))
+        lens_t.fill_(9000)
+    assert ra.sync_status() == 0
 
 
 def test_other_streams(ra, gen):
