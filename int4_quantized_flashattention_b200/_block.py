@@ -102,6 +102,11 @@ def _view(t: torch.Tensor, dtype, shape, idx: int, name: str):
                      f"{tuple(t.shape)} on {t.device}")
 
 
+def _dense(B: int, H: int, N: int, D: int, dtype, dev) -> torch.Tensor:
+    """A new dense [B, H, N, D] tensor (empty_strided takes two thirds of empty's time)."""
+    return torch.empty_strided((B, H, N, D), (H * N * D, N * D, D, 1), dtype=dtype, device=dev)
+
+
 def _cuda4(t: torch.Tensor, name: str) -> int:
     if t.dim() != 4 or not t.is_cuda:
         raise ValueError(f"{name} must be a four-dimensional CUDA tensor")
@@ -151,7 +156,7 @@ def qk_norm_rope(p: Problem, q: Optional[torch.Tensor], k: Optional[torch.Tensor
         shape = (B, H, N, D)
         qp, qs = _view(q, dt, shape, idx, "q")
         if q_out is None:
-            q_out = torch.empty(shape, dtype=_BF16, device=q.device)
+            q_out = _dense(B, H, N, D, _BF16, q.device)
             qo = q_out.data_ptr()
         else:
             qo = _arg(q_out, _BF16, shape, idx, "q_out")
@@ -162,7 +167,7 @@ def qk_norm_rope(p: Problem, q: Optional[torch.Tensor], k: Optional[torch.Tensor
         shape = (B, Hk, N, D)
         kp, ks = _view(k, dt, shape, idx, "k")
         if k_out is None:
-            k_out = torch.empty(shape, dtype=_BF16, device=k.device)
+            k_out = _dense(B, Hk, N, D, _BF16, k.device)
             ko = k_out.data_ptr()
         else:
             ko = _arg(k_out, _BF16, shape, idx, "k_out")
@@ -245,8 +250,8 @@ def kv4_read(cache: KV4Cache, block_table: torch.Tensor, start: Optional[torch.T
     B = block_table.shape[0]
     shape = (B, cache.Hk, T, cache.D)
     if out is None:
-        k, v = torch.empty(shape, dtype=dtype, device=cache.k4.device), torch.empty(shape, dtype=dtype,
-                                                                                  device=cache.k4.device)
+        dev = cache.k4.device
+        k, v = _dense(*shape, dtype, dev), _dense(*shape, dtype, dev)
     else:
         k, v = out
     b = (B,)
@@ -288,7 +293,7 @@ def attn_kv4(cache: KV4Cache, q: torch.Tensor, block_table: torch.Tensor, seq_le
                          1 if causal else 0, _scale(scale, D)))
     L = lib()
     if out is None:
-        out = torch.empty(shape, dtype=_BF16, device=q.device)
+        out = _dense(B, H, Nq, D, _BF16, q.device)
         op = out.data_ptr()
     else:
         op = _arg(out, _BF16, shape, idx, "out")
@@ -328,7 +333,7 @@ def attn_cross(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, kv_lens: Optio
     kp, ks = _view(k, _BF16, kshape, idx, "k")
     vp, vs = _view(v, _BF16, kshape, idx, "v")
     if out is None:
-        out = torch.empty(shape, dtype=_BF16, device=q.device)
+        out = _dense(B, H, Nq, D, _BF16, q.device)
     op, os_ = _view(out, _BF16, shape, idx, "out")
     rc = lib().ra_attn_cross(C.byref(_CrossProblem(B, H, Hk, Nq, Nk, D, _scale(scale, D))), qp, qs, kp, ks, vp, vs,
                              _arg(kv_lens, _I32, (B,), idx, "kv_lens"), op, os_,
