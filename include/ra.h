@@ -324,7 +324,8 @@ ra_status ra_rope_rotate_quant_noalloc(const ra_problem* p, int in_dtype,
  * ra_strides: distances in ELEMENTS between neighbours of a [B, H, N, D] tensor
  * whose D channels are contiguous; token-major projections [B, N, H, D] are
  * {N*H*D, D, H*D}.  Every stride of an extent above 1 must be at least 1 and a
- * multiple of 16 bytes; the stride of an extent of 1 is not looked at.
+ * multiple of 16 bytes; the stride of an extent of 1 is not looked at.  Calls of
+ * these operators take at most 65535 batch entries.
  */
 typedef struct {
   int64_t b, h, n;
@@ -473,7 +474,8 @@ typedef struct {
 } ra_cross_problem;
 
 /*
- *   q [B, H, Nq, D], k, v [B, Hk, Nk, D], out [B, H, Nq, D]: bf16 with strides.
+ *   q [B, H, Nq, D], k, v [B, Hk, Nk, D], out [B, H, Nq, D]: bf16 with strides;
+ *               out's are at least D, and out overlaps no input.
  *   kv_lens     [B] int32: keys of each batch entry; key and value rows behind
  *               them take no part, whatever they hold (NaN too).  NULL: all Nk.
  *               Lengths outside [0, Nk] are reported by ra_sync_status and

@@ -611,7 +611,7 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
       const size_t prow = static_cast<size_t>(it.split) * (a.nitems / (a.npairs * a.nsplit)) * a.R + at;
       // Rows leave through shared memory, kPiece bytes of each at a time, neighbouring
       // lanes a piece together: a thread writing its own row touched 32 lines per
-      // store, 7800 cycles an item at 512 keys against 1900.
+      // store, 7800 cycles an item at 512 keys against 2500.
       const uint32_t live = __ballot_sync(0xFFFFFFFFu, row_live);
       constexpr int kChunks = C::kPiece / 16, kAtOnce = 32 / kChunks;  // chunks of a piece, rows per store
       auto place = [&](int row, int ch) {  // a row's chunks lie in other banks than its neighbours'

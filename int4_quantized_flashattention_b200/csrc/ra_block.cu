@@ -50,7 +50,6 @@ bool valid_kv4_attn(const ra_kv4_cache* c, const ra_kv4_attn* a) {
   if (!c || !a || c->Hk < 1 || !valid_dim(c->D)) return false;
   if (a->B < 1 || a->H < 1 || a->Nq < 1 || a->max_len < 0 || a->H % c->Hk != 0) return false;
   if (!(a->scale > 0.0f) || !std::isfinite(a->scale) || (a->causal != 0 && a->causal != 1)) return false;
-  if (static_cast<int64_t>(a->B) * c->Hk > kMaxGrid) return false;
   return static_cast<int64_t>(a->B) * a->H * a->Nq * c->D < (1LL << 31);
 }
 
@@ -173,6 +172,9 @@ ra_status ra_attn_cross(const ra_cross_problem* p, const void* q, const ra_strid
     return RA_ERR_INVALID_ARG;
   if (!valid_strides(q_st, p->B, p->H, p->Nq, 2) || !valid_strides(k_st, p->B, p->Hk, p->Nk, 2) ||
       !valid_strides(v_st, p->B, p->Hk, p->Nk, 2) || !valid_strides(out_st, p->B, p->H, p->Nq, 2))
+    return RA_ERR_INVALID_ARG;
+  // Rows of the output must not lie over one another.
+  if ((p->B > 1 && out_st->b < p->D) || (p->H > 1 && out_st->h < p->D) || (p->Nq > 1 && out_st->n < p->D))
     return RA_ERR_INVALID_ARG;
   return from_cuda(ra::launch_attn_cross(*p, q, *q_st, k, *k_st, v, *v_st, kv_lens, out, *out_st, lse,
                                          static_cast<cudaStream_t>(stream)));

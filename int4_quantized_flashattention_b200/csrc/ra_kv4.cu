@@ -214,8 +214,8 @@ __global__ void __launch_bounds__(kRowWarps * 32) kv4_rows_kernel(const RowsArgs
   extern __shared__ __align__(128) uint8_t smem[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, q4 = lane & 3;
-  const int bh = blockIdx.z, b = bh / a.Hk, hk = bh % a.Hk;
-  const int split = blockIdx.x, r0 = blockIdx.y * 8 * NT;
+  const int bh = blockIdx.x, b = bh / a.Hk, hk = bh % a.Hk;
+  const int split = blockIdx.y, r0 = blockIdx.z * 8 * NT;
   const int R = a.G * a.Nq;
   uint32_t bad = 0;
   const int len = clamp_len(__ldg(a.seq_lens + b), a.max_pages << a.page_log2, &bad);
@@ -562,7 +562,7 @@ __global__ void __launch_bounds__(kRowWarps * 32) kv4_rows_kernel(const RowsArgs
       *reinterpret_cast<uint2*>(a.out + at * D + c) = make_uint2(pack_bf16(o.x, o.y), pack_bf16(o.z, o.w));
       if (c == 0 && a.lse) a.lse[at] = lse2 * kLn2;
     } else {
-      const size_t pr = static_cast<size_t>(split) * gridDim.z * R + at;
+      const size_t pr = static_cast<size_t>(split) * gridDim.x * R + at;
       *reinterpret_cast<float4*>(a.parts.o + pr * D + c) = o;
       if (c == 0) a.parts.lse2[pr] = lse2;
     }
@@ -717,7 +717,7 @@ cudaError_t launch_kv4_rows(const ra_kv4_cache& c, const ra_kv4_attn& at, const 
   a.Hk = c.Hk; a.G = at.H / c.Hk; a.Nq = at.Nq; a.causal = at.causal; a.nsplit = plan.nsplit;
   a.scale_log2 = at.scale * kLog2e;
   const int R = a.G * a.Nq;
-  const dim3 grid(plan.nsplit, (R + 15) / 16, at.B * c.Hk);
+  const dim3 grid(at.B * c.Hk, plan.nsplit, (R + 15) / 16);
   if (R <= 8) return c.D == 64 ? launch_rows<64, 1>(a, grid, st) : launch_rows<128, 1>(a, grid, st);
   return c.D == 64 ? launch_rows<64, 2>(a, grid, st) : launch_rows<128, 2>(a, grid, st);
 }

@@ -132,7 +132,7 @@ def _attn(ra, c=None, B=2, H=4, Nq=1, pages=4, max_len=64, causal=0, scale=0.1, 
 @pytest.mark.parametrize("kw", [dict(B=0), dict(H=3), dict(H=0), dict(Nq=0), dict(pages=0), dict(max_len=-1),
                                 dict(causal=2), dict(scale=0.0), dict(scale=-1.0), dict(scale=float("inf")),
                                 dict(q=BAD16), dict(table=None), dict(lens=None), dict(lens=BAD4), dict(qlens=BAD4),
-                                dict(out=BAD16), dict(lse=BAD4), dict(B=40000)])
+                                dict(out=BAD16), dict(lse=BAD4), dict(B=70000)])
 def test_attn_kv4_refusals(ra, kw):
     assert _attn(ra, **kw) == INVALID
 
@@ -162,7 +162,8 @@ def _cross(ra, B=2, H=4, Hk=2, Nq=9, Nk=7, D=128, scale=0.1, q=GOOD, k=GOOD, v=G
 @pytest.mark.parametrize("kw", [dict(B=0), dict(H=3), dict(Hk=0), dict(Nq=0), dict(Nk=0), dict(D=80), dict(scale=0.0),
                                 dict(scale=float("nan")), dict(q=None), dict(k=BAD16), dict(v=BAD16), dict(out=None),
                                 dict(lens=BAD4), dict(lse=BAD4), dict(qst=(4608, 1152, 0)), dict(kst=(1792, 0, 128)),
-                                dict(vst=(1792, 896, 132)), dict(ost=(0, 1152, 128)), dict(Nq=(1 << 24) + 1)])
+                                dict(vst=(1792, 896, 132)), dict(ost=(0, 1152, 128)), dict(ost=(4608, 1152, 64)), dict(ost=(4608, 120, 512)),
+                                dict(Nq=(1 << 24) + 1)])
 def test_attn_cross_refusals(ra, kw):
     assert _cross(ra, **kw) == INVALID
 

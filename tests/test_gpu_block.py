@@ -307,6 +307,25 @@ def test_attn_many_rows_split(ra, gen):
         _check_kv4(ra, c, table, lens_t, q, causal=causal)
 
 
+def test_attn_many_sequences(ra, gen):
+    """More sequence-head pairs than a grid dimension of 65535 holds, one token each."""
+    B, Hk, D = 9000, 8, 64
+    c = ra.KV4Cache.empty(B, 16, Hk, D)
+    table = torch.randperm(B, generator=gen, device="cuda")[:, None].to(torch.int32).contiguous()
+    k, v = _rand(gen, B, Hk, 16, D, dtype=torch.bfloat16), _rand(gen, B, Hk, 16, D, dtype=torch.bfloat16)
+    lens = torch.randint(0, 17, (B,), generator=gen, device="cuda").to(torch.int32)
+    ra.kv4_append(c, k, v, table, None, lens)
+    q = _rand(gen, B, Hk, 1, D, dtype=torch.bfloat16)
+    out = ra.attn_kv4(c, q, table, lens)
+    assert ra.sync_status() == 0
+    for b in (0, 1, 4095, 8190, 8191, 8192, 8999):   # on both sides of pair 65535
+        n = int(lens[b])
+        kk, vv = br.cached(c, table, b, n)
+        ref, _, bound, _ = br.attention(q[b], kk, vv, torch.full((1,), n, device="cuda"),
+                                        float(torch.tensor(D ** -0.5, dtype=torch.float32)))
+        br.assert_within(out[b], ref, bound, b)
+
+
 def test_attn_reports_bad_lengths_and_pages(ra, gen):
     for Nq in (1, 40):
         q = _rand(gen, 1, 2, Nq, 64, dtype=torch.bfloat16)
