@@ -4,10 +4,12 @@ from __future__ import annotations
 import os
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libra.so")
+BIND = os.path.join(PKG, "_bind.so")       # Python binding of part of it (CPython and torch C++ API)
 OBJDIR = os.path.join(PKG, "_build")
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
@@ -44,7 +46,26 @@ def build(force: bool = False, verbose: bool = False) -> str:
         tmp = LIB + ".tmp"
         subprocess.run(["nvcc"] + ARCH + ["-shared", "-cudart", "static", "-o", tmp] + objs, check=True)
         os.replace(tmp, LIB)
+    build_bind(force)
     return LIB
+
+
+def build_bind(force: bool = False) -> str:
+    """Compiles the binding against the installed torch and libra.so beside it."""
+    import torch
+    src = os.path.join(CSRC, "ra_bind.cpp")
+    if not force and not _newer(BIND, [src, os.path.join(os.path.dirname(PKG), "include", "ra.h")]):
+        return BIND
+    root = os.path.dirname(torch.__file__)
+    cuda = os.environ.get("CUDA_HOME", "/usr/local/cuda")
+    inc = [sysconfig.get_paths()["include"], os.path.join(root, "include"),
+           os.path.join(root, "include", "torch", "csrc", "api", "include"), os.path.join(cuda, "include")]
+    tmp = BIND + ".tmp"
+    subprocess.run(["g++", "-O2", "-std=c++20", "-shared", "-fPIC"] + [a for i in inc for a in ("-isystem", i)]
+                   + [src, "-o", tmp, "-L" + os.path.join(root, "lib"), "-ltorch_python", "-ltorch_cuda", "-ltorch_cpu",
+                      "-lc10_cuda", "-lc10", "-L" + PKG, "-l:libra.so", "-Wl,-rpath,$ORIGIN"], check=True)
+    os.replace(tmp, BIND)
+    return BIND
 
 
 if __name__ == "__main__":

@@ -178,3 +178,25 @@ def test_python_wrappers_refuse_host_tensors_and_shapes(ra):
         ra.qk_norm_rope(_problem(ra), None, None, None, None)
     with pytest.raises(ValueError):
         ra.qk_norm_rope(_problem(ra), x, None, None, None)
+
+
+def test_binding_refuses_what_is_not_a_tensor_or_structure(ra):
+    """The compiled binding's own checks: no argument reaches a C entry unchecked."""
+    bind = ra._block._bind()
+    p, x = _problem(ra), torch.zeros(1, 2, 3, 64, dtype=torch.bfloat16)
+    for bad in (None, 3, "q", [x]):
+        with pytest.raises(ValueError):
+            ra.attn_cross(bad, x, x)
+        with pytest.raises(ValueError):
+            ra.KV4Cache(bad, x, x, x)
+    with pytest.raises(ValueError):
+        ra.qk_norm_rope(p, 5, None, None, None)
+    with pytest.raises(ValueError):                       # a structure of another size
+        bind.kv4_append(b"short", 0, x, x, x, None, None)
+    with pytest.raises(TypeError):                        # no buffer at all
+        bind.kv4_append(None, 0, x, x, x, None, None)
+    for name in ("qk_norm_rope", "kv4_cache", "kv4_append", "kv4_read", "attn_kv4", "attn_cross"):
+        with pytest.raises(TypeError):
+            getattr(bind, name)()
+        with pytest.raises(TypeError):
+            getattr(bind, name)(*[x] * 20)

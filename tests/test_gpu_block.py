@@ -534,6 +534,26 @@ def test_other_streams(ra, gen):
     assert ra.sync_status() == 0
 
 
+def test_threads(ra, gen):
+    """Calls from several threads at once, each on its own stream: the results of one thread."""
+    from concurrent.futures import ThreadPoolExecutor
+    c, table, lens_t = _filled(ra, gen, [3000, 1], 64, 2, 128)
+    qs = [_rand(gen, 2, 4, n, 128, dtype=torch.bfloat16) for n in (1, 5, 60, 130)]
+    want = [ra.attn_kv4(c, q, table, lens_t, causal=True) for q in qs]
+    cross = [ra.attn_cross(q, q, q) for q in qs]
+    torch.cuda.synchronize()
+
+    def work(i):
+        with torch.cuda.stream(torch.cuda.Stream()):
+            got = [(ra.attn_kv4(c, qs[i], table, lens_t, causal=True), ra.attn_cross(qs[i], qs[i], qs[i]))
+                   for _ in range(50)]
+            torch.cuda.current_stream().synchronize()
+        return all(torch.equal(a, want[i]) and torch.equal(b, cross[i]) for a, b in got)
+    with ThreadPoolExecutor(4) as pool:
+        assert all(pool.map(work, range(4)))
+    assert ra.sync_status() == 0
+
+
 def test_wrappers_refuse(ra, gen):
     x = _rand(gen, 1, 2, 5, 64, dtype=torch.bfloat16)
     c, table, lens_t = _filled(ra, gen, [20], 16, 2, 64)
