@@ -196,13 +196,15 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
     *abort_flag = 0;
     fence_barrier_init();
   }
-  if (warp == 1) {
-    tmem_alloc(tmem_holder, 512);
-    tmem_relinquish();
-  }
   if (warp == 0 && lane == 0) {
     prefetch_tmap(&tm_q);
     if (!KV4) { prefetch_tmap(&tm_k); prefetch_tmap(&tm_v); }
+  }
+  // Before TMEM is taken: a block of the kernel before on this SM may still have to take its own.
+  grid_wait();
+  if (warp == 1) {
+    tmem_alloc(tmem_holder, 512);
+    tmem_relinquish();
   }
   tc_fence_before();
   __syncthreads();
@@ -715,8 +717,7 @@ cudaError_t launch_tiles(const CUtensorMap& mq, const CUtensorMap& mk, const CUt
   auto kern = attn_tiles_kernel<D, KV4>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
   if (e != cudaSuccess) return e;
-  kern<<<a.nitems < kNumSMs ? a.nitems : kNumSMs, C::kThreads, C::kSmem, st>>>(mq, mk, mv, a);
-  return cudaGetLastError();
+  return launch_early(kern, dim3(a.nitems < kNumSMs ? a.nitems : kNumSMs), C::kThreads, C::kSmem, st, mq, mk, mv, a);
 }
 
 }  // namespace

@@ -13,6 +13,31 @@ namespace ra {
 
 constexpr int kNumSMs = 148;  // B200: the split of a call is planned for this many SMs
 
+// Kernels of these operators start while the kernel before them in the stream ends
+// (programmatic stream serialisation): each waits for it, in every thread and before
+// it touches memory, with grid_wait(), so that a call sees what the stream's order
+// promises; grid_trigger() lets the next one start.  A launch's start and a block's
+// set-up, 1 to 2 us, then lie under the end of the call before.
+#ifdef __CUDACC__
+__device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void grid_trigger() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
+template <typename... P, typename... A>
+cudaError_t launch_early(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t st, A... args) {
+  cudaLaunchAttribute at;
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
+}
+#endif
+
 // ---------------------------------------------------------------- norm + RoPE
 struct NormRopeCall {
   const void* x[2];  // q, k (NULL: absent)

@@ -72,6 +72,8 @@ __global__ void __launch_bounds__(kThreads) kv4_append_kernel(const CacheArgs a)
   const int c0 = (lane % kLanes) * 8;
   const int which = static_cast<int>(blockIdx.y) >= a.groups ? 1 : 0;
   const int h0 = (blockIdx.y - (which ? a.groups : 0)) * a.group, h1 = min(h0 + a.group, a.Hk);
+  grid_wait();
+  grid_trigger();
   const long long row = token_row(a, t);
   // Lanes without a row (padding, no place) work on zeros and do not store.
   const size_t src = blockIdx.z * a.st[which].b + static_cast<size_t>(row < 0 ? 0 : t) * a.st[which].n + c0;
@@ -123,6 +125,8 @@ __global__ void __launch_bounds__(kThreads) kv4_read_kernel(const CacheArgs a) {
   const int c0 = (lane % kLanes) * kCh;
   const int which = static_cast<int>(blockIdx.y) >= a.groups ? 1 : 0;
   const int h0 = (blockIdx.y - (which ? a.groups : 0)) * a.group, h1 = min(h0 + a.group, a.Hk);
+  grid_wait();
+  grid_trigger();
   const long long row = token_row(a, t);
   if (row < 0) return;
 #pragma unroll 8
@@ -218,6 +222,7 @@ __global__ void __launch_bounds__(kRowWarps * 32) kv4_rows_kernel(const RowsArgs
   const int split = blockIdx.y, r0 = blockIdx.z * 8 * NT;
   const int R = a.G * a.Nq;
   uint32_t bad = 0;
+  grid_wait();
   const int len = clamp_len(__ldg(a.seq_lens + b), a.max_pages << a.page_log2, &bad);
   const int ql = a.q_lens ? clamp_len(__ldg(a.q_lens + b), a.Nq, &bad) : a.Nq;
   // Steps of this CTA: [t0, t1), every kRowWarps-th for this warp.
@@ -504,7 +509,7 @@ __global__ void __launch_bounds__(kRowWarps * 32) kv4_rows_kernel(const RowsArgs
       }
     }
   }
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  grid_trigger();
   cp_async_wait<0>();
   if (bad) atomicOr(&g_kv4_status, bad);
 
@@ -576,7 +581,8 @@ __global__ void __launch_bounds__(128) kv4_join_kernel(Kv4Parts parts, int nspli
   constexpr int kC = D / 32;
   const int lane = threadIdx.x & 31;
   const long long r = static_cast<long long>(blockIdx.x) * 4 + (threadIdx.x >> 5);
-  asm volatile("griddepcontrol.wait;" ::: "memory");  // the parts: this launch may have begun before they end
+  grid_wait();
+  grid_trigger();
   if (r >= rows) return;
   if (q_lens && static_cast<int>(r % Nq) >= __ldg(q_lens + r / rows_b)) return;
   float top = -INFINITY;
@@ -629,8 +635,7 @@ cudaError_t launch_rows(const RowsArgs& a, dim3 grid, cudaStream_t st) {
   auto kern = kv4_rows_kernel<D, NT>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, RowsCfg<D>::kSmem);
   if (e != cudaSuccess) return e;
-  kern<<<grid, kRowWarps * 32, RowsCfg<D>::kSmem, st>>>(a);
-  return cudaGetLastError();
+  return launch_early(kern, grid, kRowWarps * 32, RowsCfg<D>::kSmem, st, a);
 }
 
 }  // namespace
@@ -642,14 +647,9 @@ cudaError_t launch_kv4_append(const ra_kv4_cache& c, int dtype, int B, int T, co
   CacheArgs a = cache_args(c, B, T, table, max_pages, start, n_new, c.D / 8, &grid);
   a.x[0] = k; a.x[1] = v;
   a.st[0] = ks; a.st[1] = vs;
-  if (dtype == RA_DT_BF16) {
-    if (c.D == 64) kv4_append_kernel<true, 64><<<grid, kThreads, 0, st>>>(a);
-    else kv4_append_kernel<true, 128><<<grid, kThreads, 0, st>>>(a);
-  } else {
-    if (c.D == 64) kv4_append_kernel<false, 64><<<grid, kThreads, 0, st>>>(a);
-    else kv4_append_kernel<false, 128><<<grid, kThreads, 0, st>>>(a);
-  }
-  return cudaGetLastError();
+  auto* kern = dtype == RA_DT_BF16 ? (c.D == 64 ? kv4_append_kernel<true, 64> : kv4_append_kernel<true, 128>)
+                                   : (c.D == 64 ? kv4_append_kernel<false, 64> : kv4_append_kernel<false, 128>);
+  return launch_early(kern, grid, kThreads, 0, st, a);
 }
 
 cudaError_t launch_kv4_read(const ra_kv4_cache& c, int dtype, int B, int T, const int32_t* table, int max_pages,
@@ -657,14 +657,9 @@ cudaError_t launch_kv4_read(const ra_kv4_cache& c, int dtype, int B, int T, cons
   dim3 grid;
   CacheArgs a = cache_args(c, B, T, table, max_pages, start, n, dtype == RA_DT_BF16 ? c.D / 8 : c.D / 4, &grid);
   a.y[0] = k; a.y[1] = v;
-  if (dtype == RA_DT_BF16) {
-    if (c.D == 64) kv4_read_kernel<true, 64><<<grid, kThreads, 0, st>>>(a);
-    else kv4_read_kernel<true, 128><<<grid, kThreads, 0, st>>>(a);
-  } else {
-    if (c.D == 64) kv4_read_kernel<false, 64><<<grid, kThreads, 0, st>>>(a);
-    else kv4_read_kernel<false, 128><<<grid, kThreads, 0, st>>>(a);
-  }
-  return cudaGetLastError();
+  auto* kern = dtype == RA_DT_BF16 ? (c.D == 64 ? kv4_read_kernel<true, 64> : kv4_read_kernel<true, 128>)
+                                   : (c.D == 64 ? kv4_read_kernel<false, 64> : kv4_read_kernel<false, 128>);
+  return launch_early(kern, grid, kThreads, 0, st, a);
 }
 
 Kv4Plan kv4_plan(const ra_kv4_cache& c, const ra_kv4_attn& a) {
@@ -727,18 +722,9 @@ cudaError_t launch_kv4_join(const ra_kv4_cache& c, const ra_kv4_attn& a, const K
   const long long rows = static_cast<long long>(a.B) * a.H * a.Nq;
   const int rows_b = a.H * a.Nq;
   __nv_bfloat16* o = static_cast<__nv_bfloat16*>(out);
-  cudaLaunchAttribute at;
-  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at.val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>((rows + 3) / 4));
-  cfg.blockDim = dim3(128);
-  cfg.stream = st;
-  cfg.attrs = &at;
-  cfg.numAttrs = 1;
-  return c.D == 64
-             ? cudaLaunchKernelEx(&cfg, kv4_join_kernel<64>, parts, plan.nsplit, rows, a.Nq, rows_b, q_lens, o, lse)
-             : cudaLaunchKernelEx(&cfg, kv4_join_kernel<128>, parts, plan.nsplit, rows, a.Nq, rows_b, q_lens, o, lse);
+  const dim3 grid(static_cast<unsigned>((rows + 3) / 4));
+  return launch_early(c.D == 64 ? kv4_join_kernel<64> : kv4_join_kernel<128>, grid, 128, 0, st, parts, plan.nsplit, rows,
+                      a.Nq, rows_b, q_lens, o, lse);
 }
 
 cudaError_t read_kv4_status(uint32_t* out) {

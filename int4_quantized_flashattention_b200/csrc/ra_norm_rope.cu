@@ -65,6 +65,8 @@ __global__ void __launch_bounds__(kThreads, 3) norm_rope_kernel(const NormArgs a
   const bool in_range = n < a.N;
   const int nc = in_range ? n : a.N - 1;  // lanes past the end work on the last row and do not store
   const size_t src = blockIdx.z * a.st[which].b + nc * a.st[which].n + c0;
+  grid_wait();
+  grid_trigger();
   Raw8<kBf16> next[kAhead] = {};
 #pragma unroll
   for (int i = 0; i < kAhead; ++i)
@@ -126,9 +128,8 @@ __global__ void __launch_bounds__(kThreads, 3) norm_rope_kernel(const NormArgs a
 
 template <bool kBf16, int kD, int kRot>
 cudaError_t launch_norm(const NormArgs& a, bool layer, dim3 grid, cudaStream_t st) {
-  if (layer) norm_rope_kernel<kBf16, kD, kRot, true><<<grid, kThreads, 0, st>>>(a);
-  else norm_rope_kernel<kBf16, kD, kRot, false><<<grid, kThreads, 0, st>>>(a);
-  return cudaGetLastError();
+  return layer ? launch_early(norm_rope_kernel<kBf16, kD, kRot, true>, grid, kThreads, 0, st, a)
+               : launch_early(norm_rope_kernel<kBf16, kD, kRot, false>, grid, kThreads, 0, st, a);
 }
 
 template <bool kBf16, int kD>

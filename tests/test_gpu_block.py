@@ -534,6 +534,98 @@ def test_other_streams(ra, gen):
     assert ra.sync_status() == 0
 
 
+def _chain(ra, c, table, src, work, q_rows, steps, fence):
+    """Steps in which every call reads what the one before wrote and the next one overwrites it; `fence` runs between."""
+    B, Hk, _, D = src.shape
+    seen = []
+    for i in range(steps):
+        work.copy_(src[:, :, i:i + 1])                                        # torch before, over the last call's input
+        fence()
+        start = torch.full((B,), i, dtype=torch.int32, device="cuda")
+        ra.kv4_append(c, work, work, table, start=start)
+        fence()
+        work.zero_()
+        fence()
+        k, v = ra.kv4_read(c, table, None, i + 1)
+        fence()
+        q = k[:, :, -1:].expand(B, Hk, q_rows, D).contiguous()
+        lens_t = start + 1
+        fence()
+        o = ra.attn_kv4(c, q, table, lens_t)
+        fence()
+        x = ra.attn_cross(o, k, v, out=q)                                     # over the queries of the call before
+        fence()
+        y, _ = ra.qk_norm_rope(ra.Problem.make(B, Hk, D, SEG[D], (1, 1, 1), N=q_rows, rot=0), x, None, None, None)
+        fence()
+        seen += [k.clone(), o, x.clone(), y]
+    return seen
+
+
+@pytest.mark.parametrize("q_rows", [1, 40])
+def test_calls_in_a_row_keep_the_order_of_the_stream(ra, gen, q_rows):
+    """Kernels start before the one ahead has ended: without a wait between the calls, on the stream and captured,
+    each still sees all of what came before, and nothing of what comes after."""
+    B, Hk, D, steps = 2, 3, 128, 24
+    src = _rand(gen, B, Hk, steps, D, dtype=torch.bfloat16)
+    table = torch.randperm(B * 2, generator=gen, device="cuda").to(torch.int32).reshape(B, 2).contiguous()
+    c = ra.KV4Cache.empty(B * 2, 16, Hk, D)
+    work = torch.empty_like(src[:, :, :1])
+    args = (ra, c, table, src, work, q_rows, steps)
+    want = _chain(*args, torch.cuda.synchronize)
+    for t in (c.k4, c.sk, c.v4, c.sv):
+        t.zero_()
+    for _ in range(3):
+        got = _chain(*args, lambda: None)
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        got = _chain(*args, lambda: None)
+    for _ in range(2):
+        for t in (c.k4, c.sk, c.v4, c.sv):
+            t.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+    assert ra.sync_status() == 0
+
+
+def test_captured_over_two_streams(ra, gen):
+    """A captured call that waits for two streams at once, and one that two streams wait for."""
+    x = _rand(gen, 1, 2, 70, 64, dtype=torch.bfloat16)
+    a, b, src = torch.empty_like(x), torch.empty_like(x), x.clone()
+    side = torch.cuda.Stream()
+
+    def calls():
+        here = torch.cuda.current_stream()
+        side.wait_stream(here)
+        with torch.cuda.stream(side):
+            b.copy_(src)
+            k = ra.attn_cross(b, b, b)
+        a.copy_(src)
+        here.wait_stream(side)
+        o = ra.attn_cross(a, k, b)
+        side.wait_stream(here)
+        with torch.cuda.stream(side):
+            p = ra.attn_cross(o, o, b)
+        r = ra.attn_cross(o, k, o)
+        here.wait_stream(side)
+        return k, o, p, r
+    want = [t.clone() for t in calls()]
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        got = calls()
+    for _ in range(3):
+        a.zero_(), b.zero_()
+        for t in got:
+            t.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(u, w) for u, w in zip(got, want))
+    assert ra.sync_status() == 0
+
+
 def test_threads(ra, gen):
     """Calls from several threads at once, each on its own stream: the results of one thread."""
     from concurrent.futures import ThreadPoolExecutor
