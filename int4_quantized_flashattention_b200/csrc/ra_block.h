@@ -38,6 +38,26 @@ cudaError_t launch_early(void (*kernel)(P...), dim3 grid, int threads, size_t sm
 }
 #endif
 
+// Heads of two tensors that a CTA of a row-wise kernel walks over, for `tiles`
+// token tiles and `per_sm` CTAs at once on an SM: the waves of CTAs times their
+// length, in heads, a CTA's start counted as four of them.
+inline int heads_per_cta(long long tiles, const int* heads, int per_sm) {
+  int best = 1;
+  long long best_cost = -1;
+  for (int g = 1; g <= 64; ++g) {
+    const long long ctas = tiles * ((heads[0] + g - 1) / g + (heads[1] + g - 1) / g);
+    const long long slots = static_cast<long long>(per_sm) * kNumSMs;
+    // a grid of many waves ends as its last CTAs do: half a wave of waste at most
+    const long long cost = ctas <= 4 * slots ? (ctas + slots - 1) / slots * (g + 4) * 16
+                                             : ctas * (g + 4) * 16 / slots + (g + 4) * 8;
+    if (best_cost < 0 || cost < best_cost) {
+      best = g;
+      best_cost = cost;
+    }
+  }
+  return best;
+}
+
 // ---------------------------------------------------------------- norm + RoPE
 struct NormRopeCall {
   const void* x[2];  // q, k (NULL: absent)

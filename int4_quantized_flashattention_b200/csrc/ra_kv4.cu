@@ -18,6 +18,9 @@ namespace {
 __device__ uint32_t g_kv4_status = 0;
 
 constexpr int kThreads = 256;
+// CTAs at once on an SM (4680 tokens x 40 heads, append and read together: 65.4 us with
+// 3 and 6, 65.6 with 4 and 4, 61.7 with 4 and 6, 66.8 with 5, whose registers spill, and 6).
+constexpr int kAppendPerSm = 4, kReadPerSm = 6;
 
 // ---------------------------------------------------------------- append and read
 struct CacheArgs {
@@ -61,11 +64,22 @@ __device__ __forceinline__ long long token_row(const CacheArgs& a, int t) {
   return ((static_cast<long long>(page) * a.Hk) << a.page_log2) + (pos & ((1 << a.page_log2) - 1));
 }
 
+// The largest magnitude among eight bf16 (NaN counts for nothing, as in fmaxf).
+__device__ __forceinline__ float max_abs_bf16(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  auto mag = [](uint32_t w) {
+    w &= 0x7FFF7FFFu;
+    return *reinterpret_cast<const __nv_bfloat162*>(&w);
+  };
+  const __nv_bfloat162 m = __hmax2(__hmax2(mag(a), mag(b)), __hmax2(mag(c), mag(d)));
+  const float2 f = __bfloat1622float2(m);
+  return fmaxf(f.x, fmaxf(f.y, 0.0f));
+}
+
 // D/8 lanes per token row, eight channels each; a thread stays with one token
 // and walks over heads, so its page is looked up once, and the loads of the
 // next heads travel while it works.  Bound: HBM.
 template <bool kBf16, int kD>
-__global__ void __launch_bounds__(kThreads) kv4_append_kernel(const CacheArgs a) {
+__global__ void __launch_bounds__(kThreads, kAppendPerSm) kv4_append_kernel(const CacheArgs a) {
   constexpr int kLanes = kD / 8, kTok = 32 / kLanes, kAhead = kBf16 ? 4 : 2;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int t = (blockIdx.x * (kThreads / 32) + warp) * kTok + lane / kLanes;
@@ -84,6 +98,13 @@ __global__ void __launch_bounds__(kThreads) kv4_append_kernel(const CacheArgs a)
   };
 #pragma unroll
   for (int i = 0; i < kAhead; ++i) load(h0 + i, next[i]);
+  // The maxima of kAhead heads are reduced together: each exchange halves the heads a
+  // lane holds before it halves the lanes, so that a lane ends with one head's maximum,
+  // and one division by and one of it serve all heads (9 exchanges and 2 divisions for
+  // four heads, not 16 and 8: the kernel is bound by its instructions).
+  constexpr int kTop = kLanes / 2, kLast = kAhead == 4 ? kTop / 2 : kTop;  // lane bits that select the head
+  const bool second = (lane & kLast) != 0;
+  const int mine = (kAhead == 4 && (lane & kTop) ? 2 : 0) + (second ? 1 : 0);
   for (int hb = h0; hb < h1; hb += kAhead) {
     Raw8<kBf16> cur[kAhead];
 #pragma unroll
@@ -91,24 +112,50 @@ __global__ void __launch_bounds__(kThreads) kv4_append_kernel(const CacheArgs a)
       cur[i] = next[i];
       load(hb + kAhead + i, next[i]);
     }
+    float m[kAhead];
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      if constexpr (kBf16) {
+        const uint4 w = cur[u].u[0];
+        m[u] = max_abs_bf16(w.x, w.y, w.z, w.w);
+      } else {
+        float x[8];
+        unpack8<kBf16>(cur[u], x);
+        m[u] = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) m[u] = fmaxf(m[u], fabsf(x[i]));
+      }
+    }
+    if constexpr (kAhead == 4) {
+      const bool upper = (lane & kTop) != 0;
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const float got = __shfl_xor_sync(0xFFFFFFFFu, upper ? m[u] : m[u + 2], kTop);
+        m[u] = fmaxf(upper ? m[u + 2] : m[u], got);
+      }
+    }
+    const float got = __shfl_xor_sync(0xFFFFFFFFu, second ? m[0] : m[1], kLast);
+    float top = fmaxf(second ? m[1] : m[0], got);
+#pragma unroll
+    for (int o = kLast >> 1; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+    if (top < kKv4Tiny) top = 0.0f;  // 7 / top would leave fp32's range
+    const float inv = top == 0.0f ? 0.0f : __fdiv_rn(7.0f, top);
+    const float scale = __fdiv_rn(top, 7.0f);
+    if ((lane & (kLast - 1)) == 0 && hb + mine < h1 && row >= 0)
+      a.scale[which][static_cast<size_t>(row) + (static_cast<size_t>(hb + mine) << a.page_log2)] = scale;
 #pragma unroll
     for (int u = 0; u < kAhead; ++u) {
       const int h = hb + u;
+      const int from = (kAhead == 4 && (u & 2) ? kTop : 0) + (u & 1 ? kLast : 0);
+      const float f = __shfl_sync(0xFFFFFFFFu, inv, from, kLanes);
       float x[8];
       unpack8<kBf16>(cur[u], x);
-      float m = 0.0f;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(x[i]));
-      m = group_max(m, kLanes);
-      if (m < kKv4Tiny) m = 0.0f;  // 7 / m would leave fp32's range
-      const float inv = m == 0.0f ? 0.0f : __fdiv_rn(7.0f, m);
       uint32_t bits[8];
 #pragma unroll
-      for (int i = 0; i < 8; i += 2) quant4_bits2(x[i], x[i + 1], inv, inv, bits + i);
+      for (int i = 0; i < 8; i += 2) quant4_bits2(x[i], x[i + 1], f, f, bits + i);
       if (h < h1 && row >= 0) {
         const size_t at = static_cast<size_t>(row) + (static_cast<size_t>(h) << a.page_log2);
         *reinterpret_cast<uint32_t*>(a.codes[which] + at * (kD / 2) + (c0 >> 1)) = pack8_bits(bits);
-        if (c0 == 0) a.scale[which][at] = __fdiv_rn(m, 7.0f);
       }
     }
   }
@@ -116,10 +163,11 @@ __global__ void __launch_bounds__(kThreads) kv4_append_kernel(const CacheArgs a)
 
 // The same walk the other way.  A lane writes 16 bytes of a row, so that a
 // warp's stores are whole lines: eight bf16 channels, or four fp32 channels from
-// one half of a code word.
+// one half of a code word.  Bound: HBM, the output most of it.
 template <bool kBf16, int kD>
-__global__ void __launch_bounds__(kThreads) kv4_read_kernel(const CacheArgs a) {
+__global__ void __launch_bounds__(kThreads, kReadPerSm) kv4_read_kernel(const CacheArgs a) {
   constexpr int kCh = kBf16 ? 8 : 4, kLanes = kD / kCh, kTok = 32 / kLanes;
+  constexpr int kAhead = 4;  // heads whose loads travel while as many are written
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int t = (blockIdx.x * (kThreads / 32) + warp) * kTok + lane / kLanes;
   const int c0 = (lane % kLanes) * kCh;
@@ -129,21 +177,46 @@ __global__ void __launch_bounds__(kThreads) kv4_read_kernel(const CacheArgs a) {
   grid_trigger();
   const long long row = token_row(a, t);
   if (row < 0) return;
-#pragma unroll 8
-  for (int h = h0; h < h1; ++h) {
-    const size_t at = static_cast<size_t>(row) + (static_cast<size_t>(h) << a.page_log2);
-    const uint32_t w = __ldg(reinterpret_cast<const uint32_t*>(a.codes[which] + at * (kD / 2) + ((c0 >> 1) & ~3))) >>
-                       (4 * (c0 & 4));
-    const float s = __ldg(a.scale[which] + at);
-    float y[kCh];
+  const uint8_t* const codes = a.codes[which] + static_cast<size_t>(row) * (kD / 2) + ((c0 >> 1) & ~3);
+  const float* const scales = a.scale[which] + row;
+  uint32_t next_w[kAhead];
+  float next_s[kAhead];
+  auto load = [&](int h, uint32_t& w, float& s) {
+    w = 0;
+    s = 0.0f;
+    if (h < h1) {
+      const size_t at = static_cast<size_t>(h) << a.page_log2;
+      w = __ldg(reinterpret_cast<const uint32_t*>(codes + at * (kD / 2)));
+      s = __ldg(scales + at);
+    }
+  };
 #pragma unroll
-    for (int i = 0; i < kCh; ++i) y[i] = static_cast<float>(static_cast<int>(w << (28 - 4 * i)) >> 28) * s;
-    const size_t o = ((static_cast<size_t>(blockIdx.z) * a.Hk + h) * a.T + t) * kD + c0;
-    if constexpr (kBf16)
-      *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.y[which]) + o) =
-          make_uint4(pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3]), pack_bf16(y[4], y[5]), pack_bf16(y[6], y[7]));
-    else
-      *reinterpret_cast<float4*>(static_cast<float*>(a.y[which]) + o) = make_float4(y[0], y[1], y[2], y[3]);
+  for (int i = 0; i < kAhead; ++i) load(h0 + i, next_w[i], next_s[i]);
+  for (int hb = h0; hb < h1; hb += kAhead) {
+    uint32_t cur_w[kAhead];
+    float cur_s[kAhead];
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      cur_w[i] = next_w[i];
+      cur_s[i] = next_s[i];
+      load(hb + kAhead + i, next_w[i], next_s[i]);
+    }
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      const int h = hb + u;
+      if (h >= h1) break;
+      const uint32_t w = cur_w[u] >> (4 * (c0 & 4));
+      float y[kCh];
+#pragma unroll
+      for (int i = 0; i < kCh; ++i)
+        y[i] = static_cast<float>(static_cast<int>(w << (28 - 4 * i)) >> 28) * cur_s[u];
+      const size_t o = ((static_cast<size_t>(blockIdx.z) * a.Hk + h) * a.T + t) * kD + c0;
+      if constexpr (kBf16)
+        *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.y[which]) + o) =
+            make_uint4(pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3]), pack_bf16(y[4], y[5]), pack_bf16(y[6], y[7]));
+      else
+        *reinterpret_cast<float4*>(static_cast<float*>(a.y[which]) + o) = make_float4(y[0], y[1], y[2], y[3]);
+    }
   }
 }
 
@@ -613,7 +686,7 @@ __global__ void __launch_bounds__(128) kv4_join_kernel(Kv4Parts parts, int nspli
 int log2_of(int x) { return __builtin_ctz(static_cast<unsigned>(x)); }
 
 CacheArgs cache_args(const ra_kv4_cache& c, int B, int T, const int32_t* table, int max_pages, const int32_t* start,
-                     const int32_t* count, int lanes, dim3* grid) {
+                     const int32_t* count, int lanes, int per_sm, dim3* grid) {
   CacheArgs a{};
   a.codes[0] = c.k4; a.codes[1] = c.v4;
   a.scale[0] = c.sk; a.scale[1] = c.sv;
@@ -622,10 +695,10 @@ CacheArgs cache_args(const ra_kv4_cache& c, int B, int T, const int32_t* table, 
   a.Hk = c.Hk; a.T = T;
   const int tok = kThreads / lanes;  // tokens per CTA
   const int tiles = (T + tok - 1) / tok;
-  int group = 64;  // heads per CTA: as many as leave eight CTAs per SM, at most 64
-  while (group > 1 && static_cast<long long>(tiles) * B * 2 * ((c.Hk + group - 1) / group) < 8LL * kNumSMs) group >>= 1;
-  a.group = group;
+  const int heads[2] = {c.Hk, c.Hk};
+  const int group = heads_per_cta(static_cast<long long>(tiles) * B, heads, per_sm);
   a.groups = (c.Hk + group - 1) / group;
+  a.group = (c.Hk + a.groups - 1) / a.groups;
   *grid = dim3(tiles, 2 * a.groups, B);
   return a;
 }
@@ -644,7 +717,7 @@ cudaError_t launch_kv4_append(const ra_kv4_cache& c, int dtype, int B, int T, co
                               const void* v, const ra_strides& vs, const int32_t* table, int max_pages,
                               const int32_t* start, const int32_t* n_new, cudaStream_t st) {
   dim3 grid;
-  CacheArgs a = cache_args(c, B, T, table, max_pages, start, n_new, c.D / 8, &grid);
+  CacheArgs a = cache_args(c, B, T, table, max_pages, start, n_new, c.D / 8, kAppendPerSm, &grid);
   a.x[0] = k; a.x[1] = v;
   a.st[0] = ks; a.st[1] = vs;
   auto* kern = dtype == RA_DT_BF16 ? (c.D == 64 ? kv4_append_kernel<true, 64> : kv4_append_kernel<true, 128>)
@@ -655,7 +728,8 @@ cudaError_t launch_kv4_append(const ra_kv4_cache& c, int dtype, int B, int T, co
 cudaError_t launch_kv4_read(const ra_kv4_cache& c, int dtype, int B, int T, const int32_t* table, int max_pages,
                             const int32_t* start, const int32_t* n, void* k, void* v, cudaStream_t st) {
   dim3 grid;
-  CacheArgs a = cache_args(c, B, T, table, max_pages, start, n, dtype == RA_DT_BF16 ? c.D / 8 : c.D / 4, &grid);
+  CacheArgs a = cache_args(c, B, T, table, max_pages, start, n, dtype == RA_DT_BF16 ? c.D / 8 : c.D / 4,
+                           kReadPerSm, &grid);
   a.y[0] = k; a.y[1] = v;
   auto* kern = dtype == RA_DT_BF16 ? (c.D == 64 ? kv4_read_kernel<true, 64> : kv4_read_kernel<true, 128>)
                                    : (c.D == 64 ? kv4_read_kernel<false, 64> : kv4_read_kernel<false, 128>);

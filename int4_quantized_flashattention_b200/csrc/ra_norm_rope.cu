@@ -50,12 +50,49 @@ __device__ __forceinline__ float group_sum(float v, int lpt) {
   return v;
 }
 
+// Half rotation of the RoPE'd rows of a warp's tokens: outputs d and d + 1 are
+// the sum and the difference, over sqrt(2), of channels u and u + Dj/2 of the row
+// (RopePlan::hp), which other lanes hold.  They cross in shared memory in four planes,
+// channel e in plane e mod 4 at e / 4: a lane's u advance by four from lane to lane,
+// so that its reads are neighbours, and the tokens lie where neither reads nor writes
+// meet in a bank (rows as they are met four at a time: 48 wavefronts a head, not 16).
+template <int kD>
+struct HalfRows {
+  static constexpr int kTok = 256 / kD, kTokStride = kD / 4;
+  static constexpr int kPlane = kTok * kTokStride + (kD == 64 ? 8 : 16);
+  int put, get[4];  // get: the places of u and u + Dj/2
+  static __device__ __forceinline__ int base(int tok) {
+    return tok * kTokStride + (kD == 64 ? (tok >> 1) * 8 : tok * 16);
+  }
+  __device__ __forceinline__ void init(const RopePlan& rp, int tok, int c0) {
+    put = base(tok) + (c0 >> 2);
+#pragma unroll
+    for (int p = 0; p < 4; ++p) {
+      const int u = (rp.hp[p] & 0xFFFFu) >> 2, w = rp.hp[p] >> 18;
+      get[p] = ((u & 3) * kPlane + base(tok) + (u >> 2)) | ((w & 3) * kPlane + base(tok) + (w >> 2)) << 16;
+    }
+  }
+  __device__ __forceinline__ void apply(float* row, float* x) const {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) *reinterpret_cast<float2*>(row + i * kPlane + put) = make_float2(x[i], x[i + 4]);
+    __syncwarp();
+#pragma unroll
+    for (int p = 0; p < 4; ++p) {
+      const float u = row[get[p] & 0xFFFF], w = row[get[p] >> 16];
+      x[2 * p] = __fmul_rn(__fadd_rn(u, w), 0.70710678118654752440f);
+      x[2 * p + 1] = __fmul_rn(__fsub_rn(u, w), 0.70710678118654752440f);
+    }
+    __syncwarp();
+  }
+};
+
 // kRot: the rotation, or -1 for the norm alone.
 template <bool kBf16, int kD, int kRot, bool kLayer>
 __global__ void __launch_bounds__(kThreads, 3) norm_rope_kernel(const NormArgs a) {
   constexpr int kLanes = kD / 8, kTok = 32 / kLanes;  // lanes per row, tokens per warp
   constexpr int kAhead = kBf16 ? 4 : 2;  // heads whose loads travel while as many are worked on
-  __shared__ float rows[kRot == RA_ROT_HALF ? kThreads / 32 : 1][kRot == RA_ROT_HALF ? kAhead : 1][kTok][kD];
+  constexpr bool kHalf = kRot == RA_ROT_HALF;
+  __shared__ __align__(16) float rows[kHalf ? kThreads / 32 : 1][kHalf ? kAhead : 1][kHalf ? 4 * HalfRows<kD>::kPlane : 4];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int tok = lane / kLanes, c0 = (lane % kLanes) * 8;
   const int which = static_cast<int>(blockIdx.y) >= a.groups_q ? 1 : 0;
@@ -72,9 +109,11 @@ __global__ void __launch_bounds__(kThreads, 3) norm_rope_kernel(const NormArgs a
   for (int i = 0; i < kAhead; ++i)
     if (h0 + i < h1) load_raw8<kBf16>(a.x[which], src + (h0 + i) * a.st[which].h, next[i]);
   RopePlan rp;
+  HalfRows<kD> half;
   float2 cf[4];
   if constexpr (kRot >= 0) {
     rp.init(a.s, c0);
+    if constexpr (kHalf) half.init(rp, tok, c0);
     int gp[3];
 #pragma unroll
     for (int j = 0; j < 3; ++j) gp[j] = __ldg(a.pos + 3 * nc + j);
@@ -114,7 +153,8 @@ __global__ void __launch_bounds__(kThreads, 3) norm_rope_kernel(const NormArgs a
       const float r = rsqrtf(fmaf(group_sum(ss, kLanes), 1.0f / kD, a.eps));
 #pragma unroll
       for (int i = 0; i < 8; ++i) x[i] = fmaf(x[i] * r, w[i], b[i]);
-      if constexpr (kRot >= 0) rope_apply8(a.s, rp, kRot, cf, c0, x, rows[kRot == RA_ROT_HALF ? warp : 0][kRot == RA_ROT_HALF ? u : 0][tok]);
+      if constexpr (kRot >= 0) rope_apply8(a.s, rp, kHalf ? RA_ROT_NONE : kRot, cf, c0, x, nullptr);
+      if constexpr (kHalf) half.apply(rows[warp][u], x);
       uint32_t o[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -141,25 +181,6 @@ cudaError_t launch_rot(const NormArgs& a, int rot, bool layer, dim3 grid, cudaSt
     case RA_ROT_FULL: return launch_norm<kBf16, kD, RA_ROT_FULL>(a, layer, grid, st);
     default: return launch_norm<kBf16, kD, -1>(a, layer, grid, st);
   }
-}
-
-// Heads of two tensors that a CTA of a row-wise kernel walks over, for `tiles`
-// token tiles and `per_sm` CTAs at once on an SM: the waves of CTAs times their
-// length, in heads, a CTA's start counted as four of them.
-int heads_per_cta(long long tiles, const int* heads, int per_sm) {
-  int best = 1;
-  long long best_cost = -1;
-  for (int g = 1; g <= 64; ++g) {
-    const long long ctas = tiles * ((heads[0] + g - 1) / g + (heads[1] + g - 1) / g);
-    const long long slots = static_cast<long long>(per_sm) * kNumSMs;
-    // a grid of many waves ends as its last CTAs do: half a wave of waste at most
-    const long long cost = ctas <= 4 * slots ? (ctas + slots - 1) / slots * (g + 4) * 16 : ctas * (g + 4) * 16 / slots + (g + 4) * 8;
-    if (best_cost < 0 || cost < best_cost) {
-      best = g;
-      best_cost = cost;
-    }
-  }
-  return best;
 }
 
 }  // namespace
