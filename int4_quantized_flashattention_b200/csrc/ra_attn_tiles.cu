@@ -19,7 +19,9 @@
 // 8192 keys, 1 % faster at 512), P beside S so that S(g + 1) need not wait for
 // P V(g - 1) (4 % slower), 16 softmax warps (6 % slower, 20 % for the cache), four warps
 // of their own for the output (6 % slower at 8192 keys, 3 % faster at 512), two blocks' S by one
-// product with N = 128, which reads Q half as often but waits for both P V (24 % slower).
+// product with N = 128, which reads Q half as often but waits for both P V (24 % slower),
+// an item's output after the exponentials of the next one's first block (3 % slower at 512
+// keys, 25 % at 128), one tile half an item behind the other (2 to 3 % slower).
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <cuda_bf16.h>

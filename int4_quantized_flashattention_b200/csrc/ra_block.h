@@ -17,7 +17,9 @@ constexpr int kNumSMs = 148;  // B200: the split of a call is planned for this m
 // (programmatic stream serialisation): each waits for it, in every thread and before
 // it touches memory, with grid_wait(), so that a call sees what the stream's order
 // promises; grid_trigger() lets the next one start.  A launch's start and a block's
-// set-up, 1 to 2 us, then lie under the end of the call before.
+// set-up, 1 to 2 us, then lie under the end of the call before.  The trigger comes
+// after the wait, so that a kernel starts only when the one before the one before it has
+// ended: no line that that one left in an SM's first cache outlives the start.
 #ifdef __CUDACC__
 __device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void grid_trigger() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }

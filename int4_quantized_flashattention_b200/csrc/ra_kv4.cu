@@ -262,6 +262,10 @@ struct RowsArgs {
 constexpr int kRowWarps = 4;
 constexpr int kStep = 32;    // keys per warp and step
 constexpr int kStages = 3;
+// CTAs at once on an SM, as many as the registers allow; at D = 128 and 9 to 16 rows one
+// more than they would by themselves, for a few spilled (16 x 40 heads x 8191 keys, 16
+// rows: 235 us with two, 216 with three, 322 with four).
+template <int D, int NT> constexpr int kRowsPerSm = NT == 2 ? 3 : D == 128 ? 4 : 5;
 constexpr float kLazy = 4.0f;  // the reference maximum moves when a score passes it by this (powers of two)
 constexpr float kNone = -1e30f;  // reference of a row that has met no key: finite, so that -inf - kNone is -inf
 constexpr float kPUp = 2048.0f;  // P goes to f16 times this: at most 2^(4 + 11), below 2^-25 it loses bits
@@ -284,7 +288,7 @@ __device__ __forceinline__ int k_place(int x) { return (x & 8) | ((x & 3) << 1) 
 __device__ __forceinline__ int key_of(int g) { return (g >> 1) | ((g & 1) << 2); }
 
 template <int D, int NT>
-__global__ void __launch_bounds__(kRowWarps * 32) kv4_rows_kernel(const RowsArgs a) {
+__global__ void __launch_bounds__(kRowWarps * 32, kRowsPerSm<D, NT>) kv4_rows_kernel(const RowsArgs a) {
   using C = RowsCfg<D>;
   constexpr int kW = D / 32;        // code words of a key per lane (K)
   constexpr int kM = D / 16;        // 16-channel tiles of the output
