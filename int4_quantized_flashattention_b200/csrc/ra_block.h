@@ -40,19 +40,23 @@ cudaError_t launch_early(void (*kernel)(P...), dim3 grid, int threads, size_t sm
 }
 #endif
 
-// Heads of two tensors that a CTA of a row-wise kernel walks over, for `tiles`
-// token tiles and `per_sm` CTAs at once on an SM: the waves of CTAs times their
-// length, in heads, a CTA's start counted as four of them.
-inline int heads_per_cta(long long tiles, const int* heads, int per_sm) {
+// Heads of two tensors that a CTA of a row-wise kernel walks over, `ahead` at a time,
+// for `tiles` token tiles and `per_sm` CTAs at once on an SM: the waves of CTAs times
+// their length, a CTA's start counted as two heads, and groups of the larger tensor
+// made even.  A grid of many waves ends as its last CTAs do, half a wave of waste.  (Over
+// 14 shapes of norm + RoPE, 1 x 1560 to 1 x 32760 tokens, on average 1 % and at most 4 %
+// above the best of nine group sizes, which are up to 1.5 times apart.)
+inline int heads_per_cta(long long tiles, const int* heads, int per_sm, int ahead) {
+  const long long slots = static_cast<long long>(per_sm) * kNumSMs;
+  const int most = heads[0] > heads[1] ? heads[0] : heads[1];
   int best = 1;
   long long best_cost = -1;
-  for (int g = 1; g <= 64; ++g) {
+  for (int n = 1; n <= 64; ++n) {
+    const int groups = (most + n - 1) / n, g = (most + groups - 1) / groups;
     const long long ctas = tiles * ((heads[0] + g - 1) / g + (heads[1] + g - 1) / g);
-    const long long slots = static_cast<long long>(per_sm) * kNumSMs;
-    // a grid of many waves ends as its last CTAs do: half a wave of waste at most
-    const long long cost = ctas <= 4 * slots ? (ctas + slots - 1) / slots * (g + 4) * 16
-                                             : ctas * (g + 4) * 16 / slots + (g + 4) * 8;
-    if (best_cost < 0 || cost < best_cost) {
+    const long long waves16 = ctas <= 3 * slots ? (ctas + slots - 1) / slots * 16 : ctas * 16 / slots + 8;
+    const long long cost = waves16 * ((g + ahead - 1) / ahead * ahead + 2);
+    if (best_cost < 0 || cost <= best_cost) {  // of equal ones the fewest CTAs
       best = g;
       best_cost = cost;
     }

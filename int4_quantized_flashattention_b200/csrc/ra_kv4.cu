@@ -21,6 +21,9 @@ constexpr int kThreads = 256;
 // CTAs at once on an SM (4680 tokens x 40 heads, append and read together: 65.4 us with
 // 3 and 6, 65.6 with 4 and 4, 61.7 with 4 and 6, 66.8 with 5, whose registers spill, and 6).
 constexpr int kAppendPerSm = 4, kReadPerSm = 6;
+// Heads whose loads travel while as many are worked on.
+__host__ __device__ constexpr int append_ahead(bool bf16) { return bf16 ? 4 : 2; }
+constexpr int kReadAhead = 4;
 
 // ---------------------------------------------------------------- append and read
 struct CacheArgs {
@@ -80,7 +83,7 @@ __device__ __forceinline__ float max_abs_bf16(uint32_t a, uint32_t b, uint32_t c
 // next heads travel while it works.  Bound: HBM.
 template <bool kBf16, int kD>
 __global__ void __launch_bounds__(kThreads, kAppendPerSm) kv4_append_kernel(const CacheArgs a) {
-  constexpr int kLanes = kD / 8, kTok = 32 / kLanes, kAhead = kBf16 ? 4 : 2;
+  constexpr int kLanes = kD / 8, kTok = 32 / kLanes, kAhead = append_ahead(kBf16);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int t = (blockIdx.x * (kThreads / 32) + warp) * kTok + lane / kLanes;
   const int c0 = (lane % kLanes) * 8;
@@ -167,7 +170,6 @@ __global__ void __launch_bounds__(kThreads, kAppendPerSm) kv4_append_kernel(cons
 template <bool kBf16, int kD>
 __global__ void __launch_bounds__(kThreads, kReadPerSm) kv4_read_kernel(const CacheArgs a) {
   constexpr int kCh = kBf16 ? 8 : 4, kLanes = kD / kCh, kTok = 32 / kLanes;
-  constexpr int kAhead = 4;  // heads whose loads travel while as many are written
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int t = (blockIdx.x * (kThreads / 32) + warp) * kTok + lane / kLanes;
   const int c0 = (lane % kLanes) * kCh;
@@ -179,8 +181,8 @@ __global__ void __launch_bounds__(kThreads, kReadPerSm) kv4_read_kernel(const Ca
   if (row < 0) return;
   const uint8_t* const codes = a.codes[which] + static_cast<size_t>(row) * (kD / 2) + ((c0 >> 1) & ~3);
   const float* const scales = a.scale[which] + row;
-  uint32_t next_w[kAhead];
-  float next_s[kAhead];
+  uint32_t next_w[kReadAhead];
+  float next_s[kReadAhead];
   auto load = [&](int h, uint32_t& w, float& s) {
     w = 0;
     s = 0.0f;
@@ -191,18 +193,18 @@ __global__ void __launch_bounds__(kThreads, kReadPerSm) kv4_read_kernel(const Ca
     }
   };
 #pragma unroll
-  for (int i = 0; i < kAhead; ++i) load(h0 + i, next_w[i], next_s[i]);
-  for (int hb = h0; hb < h1; hb += kAhead) {
-    uint32_t cur_w[kAhead];
-    float cur_s[kAhead];
+  for (int i = 0; i < kReadAhead; ++i) load(h0 + i, next_w[i], next_s[i]);
+  for (int hb = h0; hb < h1; hb += kReadAhead) {
+    uint32_t cur_w[kReadAhead];
+    float cur_s[kReadAhead];
 #pragma unroll
-    for (int i = 0; i < kAhead; ++i) {
+    for (int i = 0; i < kReadAhead; ++i) {
       cur_w[i] = next_w[i];
       cur_s[i] = next_s[i];
-      load(hb + kAhead + i, next_w[i], next_s[i]);
+      load(hb + kReadAhead + i, next_w[i], next_s[i]);
     }
 #pragma unroll
-    for (int u = 0; u < kAhead; ++u) {
+    for (int u = 0; u < kReadAhead; ++u) {
       const int h = hb + u;
       if (h >= h1) break;
       const uint32_t w = cur_w[u] >> (4 * (c0 & 4));
@@ -690,7 +692,8 @@ __global__ void __launch_bounds__(128) kv4_join_kernel(Kv4Parts parts, int nspli
 int log2_of(int x) { return __builtin_ctz(static_cast<unsigned>(x)); }
 
 CacheArgs cache_args(const ra_kv4_cache& c, int B, int T, const int32_t* table, int max_pages, const int32_t* start,
-                     const int32_t* count, int lanes, int per_sm, dim3* grid) {
+                     const int32_t* count, int lanes, int per_sm, int ahead,
+                     dim3* grid) {
   CacheArgs a{};
   a.codes[0] = c.k4; a.codes[1] = c.v4;
   a.scale[0] = c.sk; a.scale[1] = c.sv;
@@ -700,9 +703,9 @@ CacheArgs cache_args(const ra_kv4_cache& c, int B, int T, const int32_t* table, 
   const int tok = kThreads / lanes;  // tokens per CTA
   const int tiles = (T + tok - 1) / tok;
   const int heads[2] = {c.Hk, c.Hk};
-  const int group = heads_per_cta(static_cast<long long>(tiles) * B, heads, per_sm);
+  const int group = heads_per_cta(static_cast<long long>(tiles) * B, heads, per_sm, ahead);
   a.groups = (c.Hk + group - 1) / group;
-  a.group = (c.Hk + a.groups - 1) / a.groups;
+  a.group = group;
   *grid = dim3(tiles, 2 * a.groups, B);
   return a;
 }
@@ -721,7 +724,8 @@ cudaError_t launch_kv4_append(const ra_kv4_cache& c, int dtype, int B, int T, co
                               const void* v, const ra_strides& vs, const int32_t* table, int max_pages,
                               const int32_t* start, const int32_t* n_new, cudaStream_t st) {
   dim3 grid;
-  CacheArgs a = cache_args(c, B, T, table, max_pages, start, n_new, c.D / 8, kAppendPerSm, &grid);
+  CacheArgs a = cache_args(c, B, T, table, max_pages, start, n_new, c.D / 8, kAppendPerSm,
+                           append_ahead(dtype == RA_DT_BF16), &grid);
   a.x[0] = k; a.x[1] = v;
   a.st[0] = ks; a.st[1] = vs;
   auto* kern = dtype == RA_DT_BF16 ? (c.D == 64 ? kv4_append_kernel<true, 64> : kv4_append_kernel<true, 128>)
@@ -733,7 +737,7 @@ cudaError_t launch_kv4_read(const ra_kv4_cache& c, int dtype, int B, int T, cons
                             const int32_t* start, const int32_t* n, void* k, void* v, cudaStream_t st) {
   dim3 grid;
   CacheArgs a = cache_args(c, B, T, table, max_pages, start, n, dtype == RA_DT_BF16 ? c.D / 8 : c.D / 4,
-                           kReadPerSm, &grid);
+                           kReadPerSm, kReadAhead, &grid);
   a.y[0] = k; a.y[1] = v;
   auto* kern = dtype == RA_DT_BF16 ? (c.D == 64 ? kv4_read_kernel<true, 64> : kv4_read_kernel<true, 128>)
                                    : (c.D == 64 ? kv4_read_kernel<false, 64> : kv4_read_kernel<false, 128>);

@@ -28,6 +28,8 @@ namespace {
 __device__ uint32_t g_norm_status = 0;
 
 constexpr int kThreads = 256;
+// Heads whose loads travel while as many are worked on.
+__host__ __device__ constexpr int ahead_of(bool bf16) { return bf16 ? 4 : 2; }
 
 struct NormArgs {
   const void* x[2];
@@ -90,7 +92,7 @@ struct HalfRows {
 template <bool kBf16, int kD, int kRot, bool kLayer>
 __global__ void __launch_bounds__(kThreads, 3) norm_rope_kernel(const NormArgs a) {
   constexpr int kLanes = kD / 8, kTok = 32 / kLanes;  // lanes per row, tokens per warp
-  constexpr int kAhead = kBf16 ? 4 : 2;  // heads whose loads travel while as many are worked on
+  constexpr int kAhead = ahead_of(kBf16);
   constexpr bool kHalf = kRot == RA_ROT_HALF;
   __shared__ __align__(16) float rows[kHalf ? kThreads / 32 : 1][kHalf ? kAhead : 1][kHalf ? 4 * HalfRows<kD>::kPlane : 4];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -204,7 +206,7 @@ cudaError_t launch_norm_rope(const ra_problem& p, const NormRopeCall& c, cudaStr
   const int tiles = (p.N + tok - 1) / tok;
   // A CTA begins with a chain of loads (positions, table), which eight heads do not
   // pay for (32760 tokens x 80 heads: 285 us against 211).
-  const int group = heads_per_cta(static_cast<long long>(tiles) * p.B, a.heads, 3);
+  const int group = heads_per_cta(static_cast<long long>(tiles) * p.B, a.heads, 3, ahead_of(c.dtype == RA_DT_BF16));
   a.group = group;
   a.groups_q = (a.heads[0] + group - 1) / group;
   const dim3 grid(tiles, a.groups_q + (a.heads[1] + group - 1) / group, p.B);
