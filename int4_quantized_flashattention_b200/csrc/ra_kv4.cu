@@ -39,27 +39,25 @@ struct CacheArgs {
   int groups, group;      // head groups per tensor, heads per group
 };
 
-// The cache row (page * Hk * page_size + slot, head 0) of this thread's token, or -1 when the
-// token is padding or has no valid place (which is reported).
-__device__ __forceinline__ long long token_row(const CacheArgs& a, int t) {
-  const int b = blockIdx.z;
-  int cnt = a.T;
-  if (a.count) {
-    cnt = __ldg(a.count + b);
-    if (cnt < 0 || cnt > a.T) {
-      atomicOr(&g_kv4_status, kStatusBadPosition);
-      return -1;
-    }
-  }
-  if (t >= cnt) return -1;
-  const int s = a.start ? __ldg(a.start + b) : 0;
+// Tokens of this CTA's sequence that the call holds; 0 for a bad count (which is reported).
+__device__ __forceinline__ int token_count(const CacheArgs& a) {
+  if (!a.count) return a.T;
+  const int cnt = __ldg(a.count + blockIdx.z);
+  if (cnt >= 0 && cnt <= a.T) return cnt;
+  atomicOr(&g_kv4_status, kStatusBadPosition);
+  return 0;
+}
+
+// The cache row (page * Hk * page_size + slot, head 0) of token t of this CTA's sequence, which
+// begins at s, or -1 when it has no valid place (which is reported).
+__device__ __forceinline__ long long token_row(const CacheArgs& a, int s, int t) {
   const long long pos = static_cast<long long>(s) + t;
   const long long pi = pos >> a.page_log2;
   if (s < 0 || pi >= a.max_pages) {
     atomicOr(&g_kv4_status, kStatusBadPosition);
     return -1;
   }
-  const int page = __ldg(a.table + static_cast<size_t>(b) * a.max_pages + pi);
+  const int page = __ldg(a.table + static_cast<size_t>(blockIdx.z) * a.max_pages + pi);
   if (page < 0 || page >= a.num_pages) {
     atomicOr(&g_kv4_status, kStatusBadPosition);
     return -1;
@@ -78,42 +76,54 @@ __device__ __forceinline__ float max_abs_bf16(uint32_t a, uint32_t b, uint32_t c
   return fmaxf(f.x, fmaxf(f.y, 0.0f));
 }
 
-// D/8 lanes per token row, eight channels each; a thread stays with one token
-// and walks over heads, so its page is looked up once, and the loads of the
-// next heads travel while it works.  Bound: HBM.
-template <bool kBf16, int kD>
+// D/8 lanes per token row, eight channels each; a thread stays with kPer tokens
+// and walks over heads, kAhead rows at a time, so its pages are looked up once, and
+// the loads of the next rows travel while it works.  kPer is 1 unless there are fewer heads
+// than rows at a time (one head of 64 channels, 12 x 3345 tokens, append and read together: 23.4
+// us with one token a thread, 13.7 with four).  Bound: HBM.
+template <bool kBf16, int kD, int kPer>
 __global__ void __launch_bounds__(kThreads, kAppendPerSm) kv4_append_kernel(const CacheArgs a) {
-  constexpr int kLanes = kD / 8, kTok = 32 / kLanes, kAhead = append_ahead(kBf16);
+  constexpr int kLanes = kD / 8, kTok = 32 / kLanes, kAhead = append_ahead(kBf16), kHeads = kAhead / kPer;
+  constexpr int kNext = kThreads / kLanes;  // from one token of a thread to the next
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int t = (blockIdx.x * (kThreads / 32) + warp) * kTok + lane / kLanes;
+  const int t = blockIdx.x * kNext * kPer + warp * kTok + lane / kLanes;
   const int c0 = (lane % kLanes) * 8;
   const int which = static_cast<int>(blockIdx.y) >= a.groups ? 1 : 0;
   const int h0 = (blockIdx.y - (which ? a.groups : 0)) * a.group, h1 = min(h0 + a.group, a.Hk);
   grid_wait();
   grid_trigger();
-  const long long row = token_row(a, t);
-  // Lanes without a row (padding, no place) work on zeros and do not store.
-  const size_t src = blockIdx.z * a.st[which].b + static_cast<size_t>(row < 0 ? 0 : t) * a.st[which].n + c0;
+  const int cnt = token_count(a);
+  const size_t src = blockIdx.z * a.st[which].b + static_cast<size_t>(t) * a.st[which].n + c0;
+  // Row i of a batch: head i / kPer, token i % kPer.  Padding is worked on as zeros.
   Raw8<kBf16> next[kAhead];
-  auto load = [&](int h, Raw8<kBf16>& r) {
-    if (h < h1 && row >= 0) load_raw8<kBf16>(a.x[which], src + h * a.st[which].h, r);
+  auto load = [&](int hb, int i, Raw8<kBf16>& r) {
+    const int h = hb + i / kPer, n = (i % kPer) * kNext;
+    if (h < h1 && t + n < cnt) load_raw8<kBf16>(a.x[which], src + h * a.st[which].h + n * a.st[which].n, r);
     else r = Raw8<kBf16>{};
   };
 #pragma unroll
-  for (int i = 0; i < kAhead; ++i) load(h0 + i, next[i]);
-  // The maxima of kAhead heads are reduced together: each exchange halves the heads a
-  // lane holds before it halves the lanes, so that a lane ends with one head's maximum,
-  // and one division by and one of it serve all heads (9 exchanges and 2 divisions for
-  // four heads, not 16 and 8: the kernel is bound by its instructions).
-  constexpr int kTop = kLanes / 2, kLast = kAhead == 4 ? kTop / 2 : kTop;  // lane bits that select the head
+  for (int i = 0; i < kAhead; ++i) load(h0, i, next[i]);
+  long long row[kPer];  // -1: not stored
+  const int s = a.start ? __ldg(a.start + blockIdx.z) : 0;
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) row[i] = t + i * kNext < cnt ? token_row(a, s, t + i * kNext) : -1;
+  // The maxima of kAhead rows are reduced together: each exchange halves the rows a
+  // lane holds before it halves the lanes, so that a lane ends with one row's maximum,
+  // and one division by and one of it serve all rows (9 exchanges and 2 divisions for
+  // four rows, not 16 and 8: the kernel is bound by its instructions).
+  constexpr int kTop = kLanes / 2, kLast = kAhead == 4 ? kTop / 2 : kTop;  // lane bits that select the row
   const bool second = (lane & kLast) != 0;
   const int mine = (kAhead == 4 && (lane & kTop) ? 2 : 0) + (second ? 1 : 0);
-  for (int hb = h0; hb < h1; hb += kAhead) {
+  long long my_row = row[0];
+#pragma unroll
+  for (int i = 1; i < kPer; ++i)
+    if (mine % kPer == i) my_row = row[i];
+  for (int hb = h0; hb < h1; hb += kHeads) {
     Raw8<kBf16> cur[kAhead];
 #pragma unroll
     for (int i = 0; i < kAhead; ++i) {
       cur[i] = next[i];
-      load(hb + kAhead + i, next[i]);
+      load(hb + kHeads, i, next[i]);
     }
     float m[kAhead];
 #pragma unroll
@@ -144,11 +154,12 @@ __global__ void __launch_bounds__(kThreads, kAppendPerSm) kv4_append_kernel(cons
     if (top < kKv4Tiny) top = 0.0f;  // 7 / top would leave fp32's range
     const float inv = top == 0.0f ? 0.0f : __fdiv_rn(7.0f, top);
     const float scale = __fdiv_rn(top, 7.0f);
-    if ((lane & (kLast - 1)) == 0 && hb + mine < h1 && row >= 0)
-      a.scale[which][static_cast<size_t>(row) + (static_cast<size_t>(hb + mine) << a.page_log2)] = scale;
+    const int my_head = hb + mine / kPer;
+    if ((lane & (kLast - 1)) == 0 && my_head < h1 && my_row >= 0)
+      a.scale[which][static_cast<size_t>(my_row) + (static_cast<size_t>(my_head) << a.page_log2)] = scale;
 #pragma unroll
     for (int u = 0; u < kAhead; ++u) {
-      const int h = hb + u;
+      const int h = hb + u / kPer;
       const int from = (kAhead == 4 && (u & 2) ? kTop : 0) + (u & 1 ? kLast : 0);
       const float f = __shfl_sync(0xFFFFFFFFu, inv, from, kLanes);
       float x[8];
@@ -156,8 +167,8 @@ __global__ void __launch_bounds__(kThreads, kAppendPerSm) kv4_append_kernel(cons
       uint32_t bits[8];
 #pragma unroll
       for (int i = 0; i < 8; i += 2) quant4_bits2(x[i], x[i + 1], f, f, bits + i);
-      if (h < h1 && row >= 0) {
-        const size_t at = static_cast<size_t>(row) + (static_cast<size_t>(h) << a.page_log2);
+      if (h < h1 && row[u % kPer] >= 0) {
+        const size_t at = static_cast<size_t>(row[u % kPer]) + (static_cast<size_t>(h) << a.page_log2);
         *reinterpret_cast<uint32_t*>(a.codes[which] + at * (kD / 2) + (c0 >> 1)) = pack8_bits(bits);
       }
     }
@@ -167,52 +178,65 @@ __global__ void __launch_bounds__(kThreads, kAppendPerSm) kv4_append_kernel(cons
 // The same walk the other way.  A lane writes 16 bytes of a row, so that a
 // warp's stores are whole lines: eight bf16 channels, or four fp32 channels from
 // one half of a code word.  Bound: HBM, the output most of it.
-template <bool kBf16, int kD>
+template <bool kBf16, int kD, int kPer>
 __global__ void __launch_bounds__(kThreads, kReadPerSm) kv4_read_kernel(const CacheArgs a) {
-  constexpr int kCh = kBf16 ? 8 : 4, kLanes = kD / kCh, kTok = 32 / kLanes;
+  constexpr int kCh = kBf16 ? 8 : 4, kLanes = kD / kCh, kTok = 32 / kLanes, kHeads = kReadAhead / kPer;
+  constexpr int kNext = kThreads / kLanes;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int t = (blockIdx.x * (kThreads / 32) + warp) * kTok + lane / kLanes;
+  const int t = blockIdx.x * kNext * kPer + warp * kTok + lane / kLanes;
   const int c0 = (lane % kLanes) * kCh;
   const int which = static_cast<int>(blockIdx.y) >= a.groups ? 1 : 0;
   const int h0 = (blockIdx.y - (which ? a.groups : 0)) * a.group, h1 = min(h0 + a.group, a.Hk);
   grid_wait();
   grid_trigger();
-  const long long row = token_row(a, t);
-  if (row < 0) return;
-  const uint8_t* const codes = a.codes[which] + static_cast<size_t>(row) * (kD / 2) + ((c0 >> 1) & ~3);
-  const float* const scales = a.scale[which] + row;
+  const int s = a.start ? __ldg(a.start + blockIdx.z) : 0;
+  const int cnt = token_count(a);
+  const uint8_t* codes[kPer];
+  const float* scales[kPer];  // NULL: not read
+  bool any = false;
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    const long long row = t + i * kNext < cnt ? token_row(a, s, t + i * kNext) : -1;
+    codes[i] = a.codes[which] + row * (kD / 2) + ((c0 >> 1) & ~3);
+    scales[i] = row < 0 ? nullptr : a.scale[which] + row;
+    any = any || row >= 0;
+  }
+  if (!any) return;
   uint32_t next_w[kReadAhead];
   float next_s[kReadAhead];
-  auto load = [&](int h, uint32_t& w, float& s) {
+  auto load = [&](int hb, int i, uint32_t& w, float& scale) {  // row i: head i / kPer, token i % kPer
+    const int h = hb + i / kPer;
     w = 0;
-    s = 0.0f;
-    if (h < h1) {
+    scale = 0.0f;
+    if (h < h1 && (kPer == 1 || scales[i % kPer])) {
       const size_t at = static_cast<size_t>(h) << a.page_log2;
-      w = __ldg(reinterpret_cast<const uint32_t*>(codes + at * (kD / 2)));
-      s = __ldg(scales + at);
+      w = __ldg(reinterpret_cast<const uint32_t*>(codes[i % kPer] + at * (kD / 2)));
+      scale = __ldg(scales[i % kPer] + at);
     }
   };
 #pragma unroll
-  for (int i = 0; i < kReadAhead; ++i) load(h0 + i, next_w[i], next_s[i]);
-  for (int hb = h0; hb < h1; hb += kReadAhead) {
+  for (int i = 0; i < kReadAhead; ++i) load(h0, i, next_w[i], next_s[i]);
+  for (int hb = h0; hb < h1; hb += kHeads) {
     uint32_t cur_w[kReadAhead];
     float cur_s[kReadAhead];
 #pragma unroll
     for (int i = 0; i < kReadAhead; ++i) {
       cur_w[i] = next_w[i];
       cur_s[i] = next_s[i];
-      load(hb + kReadAhead + i, next_w[i], next_s[i]);
+      load(hb + kHeads, i, next_w[i], next_s[i]);
     }
 #pragma unroll
     for (int u = 0; u < kReadAhead; ++u) {
-      const int h = hb + u;
+      const int h = hb + u / kPer;
       if (h >= h1) break;
+      if (kPer > 1 && !scales[u % kPer]) continue;
       const uint32_t w = cur_w[u] >> (4 * (c0 & 4));
       float y[kCh];
 #pragma unroll
       for (int i = 0; i < kCh; ++i)
         y[i] = static_cast<float>(static_cast<int>(w << (28 - 4 * i)) >> 28) * cur_s[u];
-      const size_t o = ((static_cast<size_t>(blockIdx.z) * a.Hk + h) * a.T + t) * kD + c0;
+      const size_t o =
+          ((static_cast<size_t>(blockIdx.z) * a.Hk + h) * a.T + t + (u % kPer) * kNext) * kD + c0;
       if constexpr (kBf16)
         *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.y[which]) + o) =
             make_uint4(pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3]), pack_bf16(y[4], y[5]), pack_bf16(y[6], y[7]));
@@ -693,17 +717,17 @@ int log2_of(int x) { return __builtin_ctz(static_cast<unsigned>(x)); }
 
 CacheArgs cache_args(const ra_kv4_cache& c, int B, int T, const int32_t* table, int max_pages, const int32_t* start,
                      const int32_t* count, int lanes, int per_sm, int ahead,
-                     dim3* grid) {
+                     int tokens, dim3* grid) {
   CacheArgs a{};
   a.codes[0] = c.k4; a.codes[1] = c.v4;
   a.scale[0] = c.sk; a.scale[1] = c.sv;
   a.table = table; a.start = start; a.count = count;
   a.num_pages = c.num_pages; a.page_log2 = log2_of(c.page_size); a.max_pages = max_pages;
   a.Hk = c.Hk; a.T = T;
-  const int tok = kThreads / lanes;  // tokens per CTA
+  const int tok = kThreads / lanes * tokens;  // tokens per CTA
   const int tiles = (T + tok - 1) / tok;
   const int heads[2] = {c.Hk, c.Hk};
-  const int group = heads_per_cta(static_cast<long long>(tiles) * B, heads, per_sm, ahead);
+  const int group = heads_per_cta(static_cast<long long>(tiles) * B, heads, per_sm, ahead / tokens);
   a.groups = (c.Hk + group - 1) / group;
   a.group = group;
   *grid = dim3(tiles, 2 * a.groups, B);
@@ -720,27 +744,52 @@ cudaError_t launch_rows(const RowsArgs& a, dim3 grid, cudaStream_t st) {
 
 }  // namespace
 
+namespace {
+
+using CacheKernel = void (*)(CacheArgs);
+
+// Tokens of a thread: as many as fill the rows it works on at a time.
+int tokens_per_thread(int heads, int ahead) { return heads == 1 ? ahead : heads == 2 ? ahead / 2 : 1; }
+
+template <bool kBf16, int kD>
+CacheKernel append_kernel(int tokens) {
+  if constexpr (append_ahead(kBf16) == 4)
+    if (tokens == 4) return kv4_append_kernel<kBf16, kD, 4>;
+  return tokens == 2 ? kv4_append_kernel<kBf16, kD, 2> : kv4_append_kernel<kBf16, kD, 1>;
+}
+
+template <bool kBf16, int kD>
+CacheKernel read_kernel(int tokens) {
+  return tokens == 4   ? kv4_read_kernel<kBf16, kD, 4>
+         : tokens == 2 ? kv4_read_kernel<kBf16, kD, 2>
+                       : kv4_read_kernel<kBf16, kD, 1>;
+}
+
+}  // namespace
+
 cudaError_t launch_kv4_append(const ra_kv4_cache& c, int dtype, int B, int T, const void* k, const ra_strides& ks,
                               const void* v, const ra_strides& vs, const int32_t* table, int max_pages,
                               const int32_t* start, const int32_t* n_new, cudaStream_t st) {
   dim3 grid;
+  const int tokens = tokens_per_thread(c.Hk, append_ahead(dtype == RA_DT_BF16));
   CacheArgs a = cache_args(c, B, T, table, max_pages, start, n_new, c.D / 8, kAppendPerSm,
-                           append_ahead(dtype == RA_DT_BF16), &grid);
+                           append_ahead(dtype == RA_DT_BF16), tokens, &grid);
   a.x[0] = k; a.x[1] = v;
   a.st[0] = ks; a.st[1] = vs;
-  auto* kern = dtype == RA_DT_BF16 ? (c.D == 64 ? kv4_append_kernel<true, 64> : kv4_append_kernel<true, 128>)
-                                   : (c.D == 64 ? kv4_append_kernel<false, 64> : kv4_append_kernel<false, 128>);
+  auto* kern = dtype == RA_DT_BF16 ? (c.D == 64 ? append_kernel<true, 64>(tokens) : append_kernel<true, 128>(tokens))
+                                   : (c.D == 64 ? append_kernel<false, 64>(tokens) : append_kernel<false, 128>(tokens));
   return launch_early(kern, grid, kThreads, 0, st, a);
 }
 
 cudaError_t launch_kv4_read(const ra_kv4_cache& c, int dtype, int B, int T, const int32_t* table, int max_pages,
                             const int32_t* start, const int32_t* n, void* k, void* v, cudaStream_t st) {
   dim3 grid;
+  const int tokens = tokens_per_thread(c.Hk, kReadAhead);
   CacheArgs a = cache_args(c, B, T, table, max_pages, start, n, dtype == RA_DT_BF16 ? c.D / 8 : c.D / 4,
-                           kReadPerSm, kReadAhead, &grid);
+                           kReadPerSm, kReadAhead, tokens, &grid);
   a.y[0] = k; a.y[1] = v;
-  auto* kern = dtype == RA_DT_BF16 ? (c.D == 64 ? kv4_read_kernel<true, 64> : kv4_read_kernel<true, 128>)
-                                   : (c.D == 64 ? kv4_read_kernel<false, 64> : kv4_read_kernel<false, 128>);
+  auto* kern = dtype == RA_DT_BF16 ? (c.D == 64 ? read_kernel<true, 64>(tokens) : read_kernel<true, 128>(tokens))
+                                   : (c.D == 64 ? read_kernel<false, 64>(tokens) : read_kernel<false, 128>(tokens));
   return launch_early(kern, grid, kThreads, 0, st, a);
 }
 

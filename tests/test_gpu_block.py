@@ -164,6 +164,46 @@ def test_append_and_read(ra, gen, dtype, B, Hk, D, T, page, starts, counts):
         assert torch.equal(old[m].view(torch.uint8), new[m].view(torch.uint8))
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("Hk,D", [(1, 64), (1, 128), (2, 64), (2, 128), (3, 64), (4, 128), (6, 128)])
+@pytest.mark.parametrize("T,starts,counts", [(1, (0, 17), None), (301, (5, 128), (301, 66)), (130, (63, 0), (0, 129))])
+def test_append_and_read_few_heads(ra, gen, dtype, Hk, D, T, starts, counts):
+    """A thread works on several tokens where there are fewer heads than rows at a time; a bad page among them is
+    left out alone."""
+    B, page = 2, 16
+    each = -(-(max(starts) + T) // page)
+    c, table = _make_cache(ra, gen, B, each, page, Hk, D)
+    bad_page = (starts[0] + T // 2) // page
+    table[0, bad_page] = c.num_pages                       # of the first sequence
+    before = [t.clone() for t in (c.k4, c.sk, c.v4, c.sv)]
+    k = _rand(gen, B, T, Hk, D, dtype=dtype).transpose(1, 2)
+    v = (_rand(gen, B, Hk, T, D) * torch.rand(B, Hk, T, 1, device="cuda", generator=gen) * 9).to(dtype)
+    start = torch.tensor(starts, device="cuda", dtype=torch.int32)
+    n = None if counts is None else torch.tensor(counts, device="cuda", dtype=torch.int32)
+    out = tuple(torch.full((B, Hk, T, D), 77.0, device="cuda") for _ in range(2))
+    ra.kv4_append(c, k, v, table, start, n)
+    ra.kv4_read(c, table, start, T, n, out=out)
+    written = torch.zeros(c.num_pages, Hk, page, dtype=torch.bool, device="cuda")
+    reported = 0
+    for b in range(B):
+        cnt = T if counts is None else counts[b]
+        i = torch.arange(T, device="cuda")
+        at = i + starts[b]
+        pg, slot = table[b].long()[at // page], at % page
+        good = (i < cnt) & (pg < c.num_pages)
+        reported |= int(bool(((i < cnt) & ~good).any()))
+        written[pg[good], :, slot[good]] = True
+        for x, codes, scale, y in ((k, c.k4, c.sk, out[0]), (v, c.v4, c.sv, out[1])):
+            rc, rs = br.quantise(x[b][:, good])
+            assert torch.equal(br.unpack(codes[pg[good], :, slot[good]]).transpose(0, 1), rc.long())
+            assert torch.equal(scale[pg[good], :, slot[good]].transpose(0, 1)[..., None], rs)
+            assert torch.equal(y[b][:, good], rc.float() * rs)
+            assert bool((y[b][:, ~good] == 77.0).all())
+    for old, now in zip(before, (c.k4, c.sk, c.v4, c.sv)):
+        assert torch.equal(old[~written].view(torch.uint8), now[~written].view(torch.uint8))
+    assert ra.sync_status() == reported
+
+
 def test_append_refuses_bad_places(ra, gen):
     """Pages outside the cache, positions past the table, negative starts and counts: reported, nothing written."""
     for table, start, n in (([[0, 9]], [16], None), ([[0, -1]], [16], None), ([[0, 1]], [31], None),
