@@ -258,7 +258,10 @@ __global__ void __launch_bounds__(kThreads, kReadPerSm) kv4_read_kernel(const Ca
 //     rows on one.  The channels of a k step are free to choose as long as Q
 //     uses the same: a lane's 16 bytes of a key are its four words, and the
 //     nibbles j and j + 4 of a word make an f16 pair (codes_f16_lo / _hi).
-//   * Products run in f16, in which the codes are exact.  Q's rows of the CTA are
+//   * Products run in f16, in which the codes are exact.  (As f16's subnormals
+//     2^-24 (code + 8), with 8 times Q's sum taken off beforehand, they save an
+//     operation a pair, 137 us against 144 at 16 x 40 heads x 8191 keys; but the sums
+//     then lose bits: log-sum-exp 1.3e-6 off at nine keys, 4e-8 now.)  Q's rows of the CTA are
 //     brought to a largest value of about 2^14 by a power of two: f16's 11 bits
 //     hold bf16's 8, and what lies 2^28 below the largest value loses bits.  The keys'
 //     scales multiply S in fp32.  The values' scales multiply P in fp32, relative
@@ -290,7 +293,7 @@ constexpr int kStep = 32;    // keys per warp and step
 constexpr int kStages = 3;
 // CTAs at once on an SM, as many as the registers allow; at D = 128 and 9 to 16 rows one
 // more than they would by themselves, for a few spilled (16 x 40 heads x 8191 keys, 16
-// rows: 235 us with two, 216 with three, 322 with four).
+// rows: three 8 % faster than two, four 37 % slower; 225 us).
 template <int D, int NT> constexpr int kRowsPerSm = NT == 2 ? 3 : D == 128 ? 4 : 5;
 constexpr float kLazy = 4.0f;  // the reference maximum moves when a score passes it by this (powers of two)
 constexpr float kNone = -1e30f;  // reference of a row that has met no key: finite, so that -inf - kNone is -inf
@@ -403,19 +406,15 @@ __global__ void __launch_bounds__(kRowWarps * 32, kRowsPerSm<D, NT>) kv4_rows_ke
   // 2^(14 - exponent of the largest value), within what has a normal inverse
   const int ex = max(static_cast<int>(__float_as_uint(most) >> 23), 15);
   const float q_up = __uint_as_float(static_cast<uint32_t>(min(268 - ex, 253)) << 23);
-  const float q_down = a.scale_log2 / q_up * 16777216.0f;  // the scores are multiplied with it
-  float q_off[NT][2];
+  const float q_down = a.scale_log2 / q_up;  // the scores are multiplied with it
   int lim[NT][2];
   int lim_min = len;
 #pragma unroll
   for (int j = 0; j < NT; ++j) {
-    float sum = 0.0f;
     auto pair = [&](uint32_t lo, uint32_t hi, bool odd) {  // channels c and c + 4
       const float x = __uint_as_float(odd ? lo & 0xFFFF0000u : lo << 16);
       const float y = __uint_as_float(odd ? hi & 0xFFFF0000u : hi << 16);
-      sum += x + y;
-      const float up = odd ? q_up * 0.0625f : q_up;  // the odd channels' codes come times 16
-      return pack_f16(x * up, y * up);
+      return pack_f16(x * q_up, y * q_up);
     };
 #pragma unroll
     for (int w = 0; w < kW; ++w) {
@@ -425,12 +424,6 @@ __global__ void __launch_bounds__(kRowWarps * 32, kRowsPerSm<D, NT>) kv4_rows_ke
       qf[j][2 * w + 1][0] = pair(u.y, u.w, false);  // 2, 6
       qf[j][2 * w + 1][1] = pair(u.y, u.w, true);   // 3, 7
     }
-    // The codes come as 2^-24 (code + 8): what the 8 adds is known beforehand.
-    sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 1);
-    sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 2);
-    sum *= -8.0f * q_up * 5.9604645e-8f;
-#pragma unroll
-    for (int e = 0; e < 2; ++e) q_off[j][e] = __shfl_sync(0xFFFFFFFFu, sum, (2 * q4 + e) * 4);
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
       const int rr = r0 + 8 * j + 2 * q4 + e, i = rr % a.Nq;
@@ -471,18 +464,17 @@ __global__ void __launch_bounds__(kRowWarps * 32, kRowsPerSm<D, NT>) kv4_rows_ke
       load_words<kW>(st + (16 * u + 8 + g) * C::kRow + q4 * (C::kRow / 4), w1);
 #pragma unroll
       for (int j = 0; j < NT; ++j) {
-        s[j][u][0] = s[j][u][2] = q_off[j][0];
-        s[j][u][1] = s[j][u][3] = q_off[j][1];
+        s[j][u][0] = s[j][u][1] = s[j][u][2] = s[j][u][3] = 0.0f;
       }
 #pragma unroll
       for (int w = 0; w < kW; ++w)
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
           uint32_t af[4];
-          af[0] = raw_f16_lo(w0[w] >> (8 * k));
-          af[1] = raw_f16_lo(w1[w] >> (8 * k));
-          af[2] = raw_f16_hi(w0[w] >> (8 * k));
-          af[3] = raw_f16_hi(w1[w] >> (8 * k));
+          af[0] = codes_f16_lo(w0[w] >> (8 * k));
+          af[1] = codes_f16_lo(w1[w] >> (8 * k));
+          af[2] = codes_f16_hi(w0[w] >> (8 * k));
+          af[3] = codes_f16_hi(w1[w] >> (8 * k));
 #pragma unroll
           for (int j = 0; j < NT; ++j) mma_f16(s[j][u], af, qf[j][2 * w + k][0], qf[j][2 * w + k][1]);
         }

@@ -45,12 +45,7 @@ __device__ __forceinline__ uint32_t and_xor(uint32_t a, uint32_t b, uint32_t c) 
   return d;
 }
 
-// The codes of bits 0-3 and 16-19 (or 4-7 and 20-23) as f16 pairs of 2^-24 (code + 8)
-// (or 2^-20): f16's subnormals are its integers, so the mask alone makes them.
-__device__ __forceinline__ uint32_t raw_f16_lo(uint32_t w) { return and_xor(w, 0x000F000Fu, 0x00080008u); }
-__device__ __forceinline__ uint32_t raw_f16_hi(uint32_t w) { return and_xor(w, 0x00F000F0u, 0x00800080u); }
-
-// The same as f16 pairs, from bits 0-3 and 16-19, and from bits 4-7 and 20-23: f16
+// The codes as f16 pairs, from bits 0-3 and 16-19, and from bits 4-7 and 20-23: f16
 // has ten mantissa bits, so the second pair needs no shift (1024 + 16 (code + 8),
 // times 1/16 and minus 72 in one exact fused operation).  Shifts and masks are what
 // bounds the kernels that unpack in registers: a word takes five of them, in bf16
