@@ -261,10 +261,12 @@ __global__ void __launch_bounds__(kThreads, kReadPerSm) kv4_read_kernel(const Ca
 //   * Products run in f16, in which the codes are exact.  (As f16's subnormals
 //     2^-24 (code + 8), with 8 times Q's sum taken off beforehand, they save an
 //     operation a pair, 137 us against 144 at 16 x 40 heads x 8191 keys; but the sums
-//     then lose bits: log-sum-exp 1.3e-6 off at nine keys, 4e-8 now.)  Q's rows of the CTA are
-//     brought to a largest value of about 2^14 by a power of two: f16's 11 bits
-//     hold bf16's 8, and what lies 2^28 below the largest value loses bits.  The keys'
-//     scales multiply S in fp32.  The values' scales multiply P in fp32, relative
+//     then lose bits: log-sum-exp 1.3e-6 off at nine keys, 4e-8 now.)  Each row of Q is
+//     brought to a largest value of about 2^14 by a power of two of its own: f16's 11 bits
+//     hold bf16's 8, and what lies 2^28 below the row's largest value loses bits.  (One
+//     power of two for all rows of the CTA saved four multiplications a step and made rows
+//     of zeros of those beside a much larger or an infinite one.)  The keys' scales
+//     multiply S in fp32.  The values' scales multiply P in fp32, relative
 //     to a power of two not below the largest so far (vref), so that the one
 //     rounding of P to f16 costs 2^-11 (bf16 cost 2^-8: 1.6 times the error of the
 //     output's own rounding; now none that shows).
@@ -386,9 +388,10 @@ __global__ void __launch_bounds__(kRowWarps * 32, kRowsPerSm<D, NT>) kv4_rows_ke
   // Q fragments: row 8j + g, the channels of this lane's words.
   uint32_t qf[NT][2 * kW][2];
   uint4 qraw[NT][kW];
-  float most = 0.0f;
+  float most[NT];  // of row 8j + g
 #pragma unroll
   for (int j = 0; j < NT; ++j) {
+    most[j] = 0.0f;
     const int r = r0 + 8 * j + g;
     const bool in_use = r < R && r % a.Nq < ql;
     const __nv_bfloat16* const src = a.q + (static_cast<size_t>(bh) * R + (in_use ? r : 0)) * D + q4 * (D / 4);
@@ -398,19 +401,22 @@ __global__ void __launch_bounds__(kRowWarps * 32, kRowsPerSm<D, NT>) kv4_rows_ke
       const uint32_t x[4] = {qraw[j][w].x, qraw[j][w].y, qraw[j][w].z, qraw[j][w].w};
 #pragma unroll
       for (int i = 0; i < 4; ++i)
-        most = fmaxf(most, fmaxf(fabsf(__uint_as_float(x[i] << 16)), fabsf(__uint_as_float(x[i] & 0xFFFF0000u))));
+        most[j] = fmaxf(most[j], fmaxf(fabsf(__uint_as_float(x[i] << 16)), fabsf(__uint_as_float(x[i] & 0xFFFF0000u))));
     }
   }
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) most = fmaxf(most, __shfl_xor_sync(0xFFFFFFFFu, most, o));
-  // 2^(14 - exponent of the largest value), within what has a normal inverse
-  const int ex = max(static_cast<int>(__float_as_uint(most) >> 23), 15);
-  const float q_up = __uint_as_float(static_cast<uint32_t>(min(268 - ex, 253)) << 23);
-  const float q_down = a.scale_log2 / q_up;  // the scores are multiplied with it
+  float q_down[NT][2];  // what the scores of rows 8j + 2 q4 + n are multiplied with: above zero, as -inf passes through it
   int lim[NT][2];
   int lim_min = len;
 #pragma unroll
   for (int j = 0; j < NT; ++j) {
+    most[j] = fmaxf(most[j], __shfl_xor_sync(0xFFFFFFFFu, most[j], 1));
+    most[j] = fmaxf(most[j], __shfl_xor_sync(0xFFFFFFFFu, most[j], 2));
+    // 2^(14 - exponent of the row's largest value), at most 2^100
+    const int ex = max(static_cast<int>(__float_as_uint(most[j]) >> 23), 41);
+    const float q_up = __uint_as_float(static_cast<uint32_t>(268 - ex) << 23);
+    const float down = fmaxf(a.scale_log2 / q_up, 1e-38f);
+    q_down[j][0] = __shfl_sync(0xFFFFFFFFu, down, 8 * q4);
+    q_down[j][1] = __shfl_sync(0xFFFFFFFFu, down, 8 * q4 + 4);
     auto pair = [&](uint32_t lo, uint32_t hi, bool odd) {  // channels c and c + 4
       const float x = __uint_as_float(odd ? lo & 0xFFFF0000u : lo << 16);
       const float y = __uint_as_float(odd ? hi & 0xFFFF0000u : hi << 16);
@@ -485,7 +491,7 @@ __global__ void __launch_bounds__(kRowWarps * 32, kRowsPerSm<D, NT>) kv4_rows_ke
     for (int u = 0; u < 2; ++u)
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        fk[u][e] = *reinterpret_cast<const float*>(st + C::oSk + (16 * u + 8 * e) * 4 + key_of(g) * 4) * q_down;
+        fk[u][e] = *reinterpret_cast<const float*>(st + C::oSk + (16 * u + 8 * e) * 4 + key_of(g) * 4);
         fv[u][e] = *reinterpret_cast<const float*>(st + C::oSv + (16 * u + 8 * e) * 4 + key_of(g) * 4);
       }
     if (t * kStep + kStep > lim_min) {
@@ -494,21 +500,15 @@ __global__ void __launch_bounds__(kRowWarps * 32, kRowsPerSm<D, NT>) kv4_rows_ke
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           const int key = t * kStep + key_of(g) + 16 * u + 8 * e;
-          if (key >= len) {  // slots behind the last key may hold anything: 0 * NaN is not 0
-            fk[u][e] = 1.0f;
-            fv[u][e] = 0.0f;
-          }
+          // The key's scale goes into the scores here, of the rows that see it only: a
+          // scale of zero or NaN would make NaN of the mask.
 #pragma unroll
           for (int j = 0; j < NT; ++j)
 #pragma unroll
-            for (int n = 0; n < 2; ++n)
-              if (key >= lim[j][n]) s[j][u][2 * e + n] = -INFINITY;
+            for (int n = 0; n < 2; ++n) s[j][u][2 * e + n] = key < lim[j][n] ? s[j][u][2 * e + n] * fk[u][e] : -INFINITY;
+          fk[u][e] = 1.0f;
+          if (key >= len) fv[u][e] = 0.0f;  // slots behind the last key may hold anything: 0 * NaN is not 0
         }
-      // a scale of zero would make NaN of the mask
-#pragma unroll
-      for (int u = 0; u < 2; ++u)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) fk[u][e] = fmaxf(fk[u][e], 1e-38f);
     }
     // ---- scores beside the reference, in powers of two
     float z[NT][2][4];
@@ -521,7 +521,7 @@ __global__ void __launch_bounds__(kRowWarps * 32, kRowsPerSm<D, NT>) kv4_rows_ke
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
 #pragma unroll
-          for (int n = 0; n < 2; ++n) z[j][u][2 * e + n] = fmaf(s[j][u][2 * e + n], fk[u][e], -m[j][n]);
+          for (int n = 0; n < 2; ++n) z[j][u][2 * e + n] = fmaf(s[j][u][2 * e + n], fk[u][e] * q_down[j][n], -m[j][n]);
           over = max3(over, z[j][u][2 * e], z[j][u][2 * e + 1]);
         }
     if (__any_sync(0xFFFFFFFFu, over > kLazy)) {
@@ -539,7 +539,8 @@ __global__ void __launch_bounds__(kRowWarps * 32, kRowsPerSm<D, NT>) kv4_rows_ke
         for (int n = 0; n < 2; ++n) {
           float x = kNone;
 #pragma unroll
-          for (int u = 0; u < 2; ++u) x = fmaxf(x, fmaxf(s[j][u][n] * fk[u][0], s[j][u][2 + n] * fk[u][1]));
+          for (int u = 0; u < 2; ++u)
+            x = fmaxf(x, fmaxf(s[j][u][n] * (fk[u][0] * q_down[j][n]), s[j][u][2 + n] * (fk[u][1] * q_down[j][n])));
 #pragma unroll
           for (int o = 4; o < 32; o <<= 1) x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, o));
           const float mn = fmaxf(m[j][n], x);
@@ -553,7 +554,7 @@ __global__ void __launch_bounds__(kRowWarps * 32, kRowsPerSm<D, NT>) kv4_rows_ke
 #pragma unroll
           for (int e = 0; e < 2; ++e)
 #pragma unroll
-            for (int n = 0; n < 2; ++n) z[j][u][2 * e + n] = fmaf(s[j][u][2 * e + n], fk[u][e], -m[j][n]);
+            for (int n = 0; n < 2; ++n) z[j][u][2 * e + n] = fmaf(s[j][u][2 * e + n], fk[u][e] * q_down[j][n], -m[j][n]);
 #pragma unroll
         for (int i = 0; i < kM; ++i) {
           acc[j][i][0] *= f[0];
