@@ -607,9 +607,11 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
         if (!(ok = wait_warp(pv_done + tt * 2 + ((g - 1) & 1), ((g - 1) >> 1) & 1, abort_flag))) break;
         tc_fence_after();
       }
-      const bool some = m != -INFINITY;
+      // The sum tells a row without keys (zero) from one that is not finite (NaN).  Scores of
+      // minus infinity alone, 0 / 0, leave a sum of zero too, and give NaN.
+      const bool some = l != 0.0f || (it.nb > 0 && lim > it.k0);
       const float inv = some ? (KV4 ? ex2_approx(ev - kPUp - kVUp) : 1.0f) / l : 0.0f;
-      const float lse2 = some ? m + log2f(l) : -INFINITY;
+      const float lse2 = l != 0.0f ? m + log2f(l) : -INFINITY;
       const size_t bh = static_cast<size_t>(it.b) * a.heads + it.h;
       const size_t at = bh * a.R + r;
       const bool split = KV4 && a.nsplit > 1;

@@ -655,8 +655,13 @@ __global__ void __launch_bounds__(kRowWarps * 32, kRowsPerSm<D, NT>) kv4_rows_ke
       sum = fmaf(f, rl[w * kRows + row], sum);
       o.x = fmaf(f, v.x, o.x); o.y = fmaf(f, v.y, o.y); o.z = fmaf(f, v.z, o.z); o.w = fmaf(f, v.w, o.w);
     }
-    const float inv = top == kNone ? 0.0f : 1.0f / sum;
-    const float lse2 = top == kNone ? -INFINITY : top + log2f(sum);
+    // Sums tell rows without keys (zero) from rows that are not finite (NaN).  Scores of minus
+    // infinity alone, 0 / 0, leave a sum of zero too: such a row, or such a part of it, is NaN
+    // with a log-sum-exp of -inf, which the join takes for NaN if the row has nothing else.
+    const int i = r % a.Nq;
+    const bool sees = t0 < t1 && (a.causal ? len - ql + i + 1 : len) > t0 * kStep;
+    const float inv = sum != 0.0f ? 1.0f / sum : sees ? NAN : 0.0f;
+    const float lse2 = sum != 0.0f ? top + log2f(sum) : -INFINITY;
     const size_t at = static_cast<size_t>(bh) * R + r;
     o.x *= inv; o.y *= inv; o.z *= inv; o.w *= inv;
     if (a.nsplit == 1) {
@@ -683,15 +688,19 @@ __global__ void __launch_bounds__(128) kv4_join_kernel(Kv4Parts parts, int nspli
   if (q_lens && static_cast<int>(r % Nq) >= __ldg(q_lens + r / rows_b)) return;
   float top = -INFINITY;
   for (int s = 0; s < nsplit; ++s) top = fmaxf(top, parts.lse2[s * rows + r]);
-  float sum = 0.0f, o[kC];
+  float sum = 0.0f, none = 0.0f, o[kC];
 #pragma unroll
   for (int i = 0; i < kC; ++i) o[i] = 0.0f;
 #pragma unroll 4
   for (int s = 0; s < nsplit; ++s) {
     const float x = parts.lse2[s * rows + r];
-    const float w = x == -INFINITY ? 0.0f : ex2_approx(x - top);
-    sum += w;
     const float* src = parts.o + (s * rows + r) * D + lane * kC;
+    if (x == -INFINITY) {  // no keys (zeros), or weights that are all zero (NaN)
+      none += src[0];
+      continue;
+    }
+    const float w = ex2_approx(x - top);
+    sum += w;
 #pragma unroll
     for (int i = 0; i < kC; i += 2) {
       const float2 v = *reinterpret_cast<const float2*>(src + i);
@@ -699,11 +708,11 @@ __global__ void __launch_bounds__(128) kv4_join_kernel(Kv4Parts parts, int nspli
       o[i + 1] = fmaf(w, v.y, o[i + 1]);
     }
   }
-  const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
+  const float inv = sum != 0.0f ? 1.0f / sum : none;
   uint32_t* dst = reinterpret_cast<uint32_t*>(out + r * D + lane * kC);
 #pragma unroll
   for (int i = 0; i < kC; i += 2) dst[i / 2] = pack_bf16(o[i] * inv, o[i + 1] * inv);
-  if (lse && lane == 0) lse[r] = sum > 0.0f ? (top + log2f(sum)) * kLn2 : -INFINITY;
+  if (lse && lane == 0) lse[r] = sum != 0.0f ? (top + log2f(sum)) * kLn2 : -INFINITY;
 }
 
 int log2_of(int x) { return __builtin_ctz(static_cast<unsigned>(x)); }
