@@ -375,8 +375,9 @@ ra_status ra_qk_norm_rope(const ra_problem* p, int Hk, int norm, float eps, int 
  * A paged cache of keys and values in 4 bits: per token and head the symmetric
  * INT4 codes of ra_rope_rotate_quant's Q and K rule (s = fl(amax/7), code =
  * rint(x * fl(7/amax)) of the exact product, ties to even), for K and V alike.
- * A row whose amax is below 2^-125 gets s = 0 and codes 0.  Keys go in after
- * RoPE and, where used, the rotation (queries then carry the same rotation).
+ * A row whose amax is below 2^-125 gets s = 0 and codes 0; a row that holds a
+ * NaN or an infinity gets s = NaN (its codes mean nothing), so that it is NaN
+ * wherever it is read.  Keys go in after RoPE and, where used, the rotation (queries then carry the same rotation).
  *   page_size   tokens per page: 16, 32, 64 or 128.
  *   Hk, D       heads, head dimension (64 or 128).
  *   k4, v4      [num_pages, Hk, page_size, D/2] packed codes.

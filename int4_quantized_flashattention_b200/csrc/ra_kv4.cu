@@ -65,15 +65,22 @@ __device__ __forceinline__ long long token_row(const CacheArgs& a, int s, int t)
   return ((static_cast<long long>(page) * a.Hk) << a.page_log2) + (pos & ((1 << a.page_log2) - 1));
 }
 
-// The largest magnitude among eight bf16 (NaN counts for nothing, as in fmaxf).
+// The larger one, NaN if either is.
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+  return d;
+}
+
+// The largest magnitude among eight bf16, NaN if one of them is.
 __device__ __forceinline__ float max_abs_bf16(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
   auto mag = [](uint32_t w) {
     w &= 0x7FFF7FFFu;
     return *reinterpret_cast<const __nv_bfloat162*>(&w);
   };
-  const __nv_bfloat162 m = __hmax2(__hmax2(mag(a), mag(b)), __hmax2(mag(c), mag(d)));
+  const __nv_bfloat162 m = __hmax2_nan(__hmax2_nan(mag(a), mag(b)), __hmax2_nan(mag(c), mag(d)));
   const float2 f = __bfloat1622float2(m);
-  return fmaxf(f.x, fmaxf(f.y, 0.0f));
+  return max_nan(f.x, f.y);
 }
 
 // D/8 lanes per token row, eight channels each; a thread stays with kPer tokens
@@ -136,7 +143,7 @@ __global__ void __launch_bounds__(kThreads, kAppendPerSm) kv4_append_kernel(cons
         unpack8<kBf16>(cur[u], x);
         m[u] = 0.0f;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) m[u] = fmaxf(m[u], fabsf(x[i]));
+        for (int i = 0; i < 8; ++i) m[u] = max_nan(m[u], fabsf(x[i]));
       }
     }
     if constexpr (kAhead == 4) {
@@ -144,13 +151,16 @@ __global__ void __launch_bounds__(kThreads, kAppendPerSm) kv4_append_kernel(cons
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
         const float got = __shfl_xor_sync(0xFFFFFFFFu, upper ? m[u] : m[u + 2], kTop);
-        m[u] = fmaxf(upper ? m[u + 2] : m[u], got);
+        m[u] = max_nan(upper ? m[u + 2] : m[u], got);
       }
     }
     const float got = __shfl_xor_sync(0xFFFFFFFFu, second ? m[0] : m[1], kLast);
-    float top = fmaxf(second ? m[1] : m[0], got);
+    float top = max_nan(second ? m[1] : m[0], got);
 #pragma unroll
-    for (int o = kLast >> 1; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+    for (int o = kLast >> 1; o > 0; o >>= 1) top = max_nan(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+    // What is not finite stays so: the row's scale is NaN, whatever its codes then are.  (Codes of zeros
+    // took a test and a selection a row: 23.9 us against 21.9 for 40 heads x 4680 tokens.)
+    if (top == INFINITY) top = NAN;
     if (top < kKv4Tiny) top = 0.0f;  // 7 / top would leave fp32's range
     const float inv = top == 0.0f ? 0.0f : __fdiv_rn(7.0f, top);
     const float scale = __fdiv_rn(top, 7.0f);
