@@ -277,9 +277,10 @@ __global__ void __launch_bounds__(kThreads, kReadPerSm) kv4_read_kernel(const Ca
 //     power of two for all rows of the CTA saved four multiplications a step and made rows
 //     of zeros of those beside a much larger or an infinite one.)  The keys' scales
 //     multiply S in fp32.  The values' scales multiply P in fp32, relative
-//     to a power of two not below the largest so far (vref), so that the one
+//     to a power of two not below the largest that the row has seen so far, so that the one
 //     rounding of P to f16 costs 2^-11 (bf16 cost 2^-8: 1.6 times the error of the
-//     output's own rounding; now none that shows).
+//     output's own rounding; now none that shows).  Below 2^-25 of it a product loses
+//     bits.  Keys that a row does not see leave its reference alone, whatever they hold.
 //   * O^T = V^T P^T, again 16 channels by 8 rows: P^T comes out of S^T by one
 //     8x8 transpose per 8 keys, V^T by pairing the words of two keys.  The
 //     pairs are keys x and x + 4 of each eight, which puts the rows that the
@@ -310,6 +311,7 @@ template <int D, int NT> constexpr int kRowsPerSm = NT == 2 ? 3 : D == 128 ? 4 :
 constexpr float kLazy = 4.0f;  // the reference maximum moves when a score passes it by this (powers of two)
 constexpr float kNone = -1e30f;  // reference of a row that has met no key: finite, so that -inf - kNone is -inf
 constexpr float kPUp = 2048.0f;  // P goes to f16 times this: at most 2^(4 + 11), below 2^-25 it loses bits
+constexpr uint32_t kPUpBits = (127u + 127 + 11) << 23;  // less the bits of a power of two: those of kPUp over it
 
 template <int D>
 struct RowsCfg {
@@ -450,9 +452,12 @@ __global__ void __launch_bounds__(kRowWarps * 32, kRowsPerSm<D, NT>) kv4_rows_ke
 
   float acc[NT][kM][4];
   float m[NT][2], l[NT][2];
-  float vref = 9.8607613e-32f, vinv = kPUp / vref;  // from 2^-103
+  constexpr float kVStart = 9.8607613e-32f;  // 2^-103
+  float vinv[NT][2];      // kPUp over each row's reference of the values' scales
+  float vlim = kVStart;   // the smallest reference of this lane's rows
 #pragma unroll
   for (int j = 0; j < NT; ++j) {
+    vinv[j][0] = vinv[j][1] = kPUp / kVStart;
 #pragma unroll
     for (int i = 0; i < kM; ++i)
 #pragma unroll
@@ -522,8 +527,8 @@ __global__ void __launch_bounds__(kRowWarps * 32, kRowsPerSm<D, NT>) kv4_rows_ke
     }
     // ---- scores beside the reference, in powers of two
     float z[NT][2][4];
-    const float fv_top = max3(fv[0][0], fv[0][1], fmaxf(fv[1][0], fv[1][1]));
-    float over = fv_top > vref ? 1e30f : 0.0f;
+    const float fv_top = max_nan(max_nan(fabsf(fv[0][0]), fabsf(fv[0][1])), max_nan(fabsf(fv[1][0]), fabsf(fv[1][1])));
+    float over = fv_top <= vlim ? 0.0f : 1e30f;  // NaN and infinities too
 #pragma unroll
     for (int j = 0; j < NT; ++j)
 #pragma unroll
@@ -535,13 +540,7 @@ __global__ void __launch_bounds__(kRowWarps * 32, kRowsPerSm<D, NT>) kv4_rows_ke
           over = max3(over, z[j][u][2 * e], z[j][u][2 * e + 1]);
         }
     if (__any_sync(0xFFFFFFFFu, over > kLazy)) {
-      float v = fv_top;
-#pragma unroll
-      for (int o = 4; o < 32; o <<= 1) v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, o));
-      v = fmaxf(vref, __uint_as_float((__float_as_uint(v) + 0x007FFFFFu) & 0x7F800000u));  // a power of two
-      const float fr = vref / v;
-      vref = v;
-      vinv = kPUp / v;
+      vlim = INFINITY;
 #pragma unroll
       for (int j = 0; j < NT; ++j) {
         float f[2];
@@ -557,7 +556,22 @@ __global__ void __launch_bounds__(kRowWarps * 32, kRowsPerSm<D, NT>) kv4_rows_ke
           f[n] = ex2_approx(m[j][n] - mn);
           m[j][n] = mn;
           l[j][n] *= f[n];
-          f[n] *= fr;
+          // The same for the values' scales; a value that is not finite makes NaN of the
+          // rows that see it, and is left out of the products.
+          uint32_t v = 0;  // magnitudes compare like their bits, what is not finite above all others
+#pragma unroll
+          for (int u = 0; u < 2; ++u)
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+              if (s[j][u][2 * e + n] != -INFINITY) v = max(v, __float_as_uint(fv[u][e]) & 0x7FFFFFFFu);
+#pragma unroll
+          for (int o = 4; o < 32; o <<= 1) v = max(v, __shfl_xor_sync(0xFFFFFFFFu, v, o));
+          const bool spoiled = v >= 0x7F800000u;
+          const uint32_t was = kPUpBits - __float_as_uint(vinv[j][n]);  // powers of two: differences of bits
+          const uint32_t now = spoiled ? was : max(was, (v + 0x007FFFFFu) & 0x7F800000u);
+          vinv[j][n] = __uint_as_float(kPUpBits - now);
+          vlim = fminf(vlim, __uint_as_float(now));
+          f[n] *= spoiled ? NAN : __uint_as_float(was) * __uint_as_float(0x7F000000u - now);
         }
 #pragma unroll
         for (int u = 0; u < 2; ++u)
@@ -573,6 +587,10 @@ __global__ void __launch_bounds__(kRowWarps * 32, kRowsPerSm<D, NT>) kv4_rows_ke
           acc[j][i][3] *= f[1];
         }
       }
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) fv[u][e] = fabsf(fv[u][e]) < INFINITY ? fv[u][e] : 0.0f;
     }
     // ---- P^T (times the values' scales) and O^T
 #pragma unroll
@@ -580,13 +598,13 @@ __global__ void __launch_bounds__(kRowWarps * 32, kRowsPerSm<D, NT>) kv4_rows_ke
       uint32_t pb[NT][2];
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        const float fr = fv[u][e] * vinv;
 #pragma unroll
         for (int j = 0; j < NT; ++j) {
           const float p0 = ex2_approx(z[j][u][2 * e]), p1 = ex2_approx(z[j][u][2 * e + 1]);
           l[j][0] += p0;
           l[j][1] += p1;
-          pb[j][e] = transpose8(pack_f16(p0 * fr, p1 * fr));
+          // in this order: zero times the scale of a key that the row does not see stays zero
+          pb[j][e] = transpose8(pack_f16(p0 * fv[u][e] * vinv[j][0], p1 * fv[u][e] * vinv[j][1]));
         }
       }
       constexpr int kVW = D / 64;  // code words of a key per lane (V)
@@ -638,7 +656,7 @@ __global__ void __launch_bounds__(kRowWarps * 32, kRowsPerSm<D, NT>) kv4_rows_ke
     for (int i = 0; i < kM; ++i)
 #pragma unroll
       for (int e = 0; e < 4; ++e)
-        ro[(warp * kRows + 8 * j + 2 * q4 + (e & 1)) * D + g * (D / 8) + i + (e >> 1) * kM] = acc[j][i][e] * (vref / kPUp);
+        ro[(warp * kRows + 8 * j + 2 * q4 + (e & 1)) * D + g * (D / 8) + i + (e >> 1) * kM] = acc[j][i][e] * __uint_as_float(0x7F000000u - __float_as_uint(vinv[j][e & 1]));
     if (g == 0) {
 #pragma unroll
       for (int n = 0; n < 2; ++n) {
