@@ -47,6 +47,15 @@ template <bool KV4> constexpr float kLazy = KV4 ? 4.0f : 8.0f;
 constexpr float kPUp = 11.0f;  // cache: P goes to f16 times 2^kPUp, at most 2^15
 constexpr int kVUp = 12;       // and the values times 2^kVUp, at most 7 * 2^12: a scale keeps its bits down to
                                // 2^-26 of the largest of its 32 keys
+// Under a causal mask, values of 32 keys whose scales are further apart than 2^kApart, or not
+// finite, go to the products as codes, and their scales into P of each row, relative to the
+// largest that the row sees: with one exponent for all rows, keys that a row does not see would
+// take its bits.  A form of the kernel by itself, as what looks for such values costs where
+// there are none (a frame of 1560 rows over 32760 keys, causal and not: 1405 and 1366 us at
+// D = 128, 1396 and 1210 at D = 64).
+constexpr int kApart = 8;
+constexpr float kOdd = -200.0f, kUnseen = -150.0f;  // in place of an exponent (which is at least -100)
+constexpr float kNoSum = 140.0f;                    // a shift whose inverse, 2^-140, is zero
 
 template <int D, bool KV4>
 struct CfgT {
@@ -59,8 +68,9 @@ struct CfgT {
   static constexpr int oQ = 0;
   static constexpr int oK = oQ + kTiles * kQBytes;
   static constexpr int oV = oK + kStages * kKVBytes;
-  static constexpr int oScale = oV + kStages * kKVBytes;      // [sk | sv][stage][key], cache only
-  static constexpr int oStage = oScale + (KV4 ? 2 * kStages * kKeys * 4 : 0);  // [softmax warp][row][kPiece]
+  static constexpr int oScale = oV + kStages * kKVBytes;      // [sk | log2 sv][stage][key], cache only
+  static constexpr int oVExp = oScale + (KV4 ? 2 * kStages * kKeys * 4 : 0);   // [stage][half]: exponents, then masks
+  static constexpr int oStage = oVExp + (KV4 ? 128 : 0);                       // [softmax warp][row][kPiece]
   static constexpr int kPiece = KV4 ? 64 : 128;        // bytes of a row that leave at a time
   static constexpr int oBar = oStage + 8 * 32 * kPiece;
   static constexpr int kNumBars = 2 + 2 + 5 * kStages + 4 + 4 + 4 + 2;
@@ -96,7 +106,7 @@ struct TileArgs {
   const float* sk;
   const uint8_t* v4;
   const float* sv;
-  int num_pages, page_log2, max_pages, Nq, causal;
+  int num_pages, page_log2, max_pages, Nq;
   Kv4Parts parts;
 };
 
@@ -106,7 +116,7 @@ struct Item {
   int k0, nb;       // first key and number of the item's key blocks
 };
 
-template <bool KV4>
+template <bool KV4, bool MASK>
 __device__ __forceinline__ Item get_item(const TileArgs& a, int item, uint32_t* bad) {
   Item it;
   const int pair = item % a.npairs, rest = item / a.npairs;
@@ -121,7 +131,7 @@ __device__ __forceinline__ Item get_item(const TileArgs& a, int item, uint32_t* 
     it.len = clamp_len(__ldg(a.kv_lens + it.b), a.max_pages << a.page_log2, bad);
     it.ql = a.q_lens ? clamp_len(__ldg(a.q_lens + it.b), a.Nq, bad) : a.Nq;
     end = it.len;
-    if (a.causal) {  // the furthest key that a row of the item sees
+    if constexpr (MASK) {  // the furthest key that a row of the item sees
       const int last = min(it.row0 + kTiles * kRows, a.R) - 1;
       if (it.row0 / a.Nq == last / a.Nq) end = max(0, min(end, it.len - it.ql + last % a.Nq + 1));
     }
@@ -164,7 +174,8 @@ __device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, volati
 
 __device__ __forceinline__ float max3t(float a, float b, float c) { return fmaxf(a, fmaxf(b, c)); }
 
-template <int D, bool KV4>
+// MASK: causal (cache only).
+template <int D, bool KV4, bool MASK>
 __global__ void __launch_bounds__(CfgT<D, KV4>::kThreads, 1)
 attn_tiles_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                   const __grid_constant__ CUtensorMap tm_v, const TileArgs a) {
@@ -214,7 +225,9 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
   tc_fence_after();
   const uint32_t tbase = *tmem_holder;
   float* const scales = reinterpret_cast<float*>(smem + C::oScale);  // cache: of the keys
-  float* const v_exp = scales + C::kStages * kKeys;                   // cache: exponents of the values' scales
+  float* const v_log = scales + C::kStages * kKeys;                   // cache: log2 of the values' scales, kOdd only
+  float* const v_exp = reinterpret_cast<float*>(smem + C::oVExp);     // cache: exponents of the values' scales
+  uint32_t* const v_bad = reinterpret_cast<uint32_t*>(v_exp + 2 * C::kStages);  // keys not finite, kOdd only
   uint32_t bad = 0;
   bool ok = true;
   if (warp < 4) {
@@ -225,7 +238,7 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
       // ------------------------------------------------------------ TMA producer
       uint32_t g = 0, li = 0;
       for (int item = blockIdx.x; item < a.nitems && ok; item += gridDim.x) {
-        const Item it = get_item<KV4>(a, item, &bad);
+        const Item it = get_item<KV4, MASK>(a, item, &bad);
         if (it.nb == 0) continue;
         auto load_q = [&]() {
           for (int tt = 0; tt < kTiles && ok; ++tt) {
@@ -295,7 +308,7 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
         return true;
       };
       for (int item = blockIdx.x; item < a.nitems && ok; item += gridDim.x) {
-        const Item it = get_item<KV4>(a, item, &bad);
+        const Item it = get_item<KV4, MASK>(a, item, &bad);
         if (it.nb == 0) continue;
         if (!(ok = wait_t(q_full + tt, li & 1, abort_flag))) break;
         ++li;
@@ -323,7 +336,7 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
       // ------------------------------------------------------------ value rows behind the last key
       uint32_t g = 0;
       for (int item = blockIdx.x; item < a.nitems && ok; item += gridDim.x) {
-        const Item it = get_item<KV4>(a, item, &bad);
+        const Item it = get_item<KV4, MASK>(a, item, &bad);
         for (int t = 0; t < it.nb; ++t, ++g) {
           const int s = g % C::kStages;
           if (!(ok = wait_warp(v_full + s, (g / C::kStages) & 1, abort_flag))) break;
@@ -401,11 +414,18 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
       // channels 0 4 1 5 2 6 3 7 of eight, which the output puts right.
       auto put_values = [&](const uint4* code, float scale, uint32_t g) -> bool {
         const int s = g % C::kStages;
-        float vm = scale;
+        float vm = fabsf(scale);
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) vm = fmaxf(vm, __shfl_xor_sync(0xFFFFFFFFu, vm, o));
+        for (int o = 16; o > 0; o >>= 1) vm = max_nan(vm, __shfl_xor_sync(0xFFFFFFFFu, vm, o));
         const uint32_t ve = min(max((__float_as_uint(vm) + 0x007FFFFFu) >> 23, 27u), 253u);  // 2^(ve - 127)
-        const __half2 v_scale = __float2half2_rn(scale * __uint_as_float((254u + kVUp - ve) << 23));
+        float v_up = scale * __uint_as_float((254u + kVUp - ve) << 23), e = static_cast<float>(ve) - 127.0f;
+        if constexpr (MASK) {
+          if (__any_sync(0xFFFFFFFFu, (scale != 0.0f && fabsf(scale) * (1 << kApart) < vm) || !(vm < INFINITY))) {
+            v_up = copysignf(1 << kVUp, scale);
+            e = kOdd;
+          }
+        }
+        const __half2 v_scale = __float2half2_rn(v_up);
         auto times = [&](uint32_t x) {
           const __half2 r = __hmul2(*reinterpret_cast<const __half2*>(&x), v_scale);
           return *reinterpret_cast<const uint32_t*>(&r);
@@ -423,7 +443,15 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
             *reinterpret_cast<uint4*>(vt + (ch >> 3) * C::kHalf + (((ch & 7) ^ (row & 7)) << 4)) = o;
           }
         }
-        if (part == 0 && lane == 0) v_exp[s * 2 + (row >> 5)] = static_cast<float>(ve) - 127.0f;
+        if (part == 0 && lane == 0) v_exp[s * 2 + (row >> 5)] = e;
+        if constexpr (MASK) {
+          if (part == 0 && e == kOdd) {
+            const bool finite = fabsf(scale) < INFINITY;
+            v_log[s * kKeys + row] = finite ? __log2f(fabsf(scale)) : -INFINITY;
+            const uint32_t bad_keys = ~__ballot_sync(0xFFFFFFFFu, finite);
+            if (lane == 0) v_bad[s * 2 + (row >> 5)] = bad_keys;
+          }
+        }
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(v_ready + s);
@@ -431,7 +459,7 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
       };
       uint32_t g = 0;
       for (int item = blockIdx.x; item < a.nitems && ok; item += gridDim.x) {
-        const Item it = get_item<KV4>(a, item, &bad);
+        const Item it = get_item<KV4, MASK>(a, item, &bad);
         // The codes of the next block travel while this one's are unpacked.
         if constexpr (C::kTwoUnpack) {
           const bool of_keys = warp < 8;  // warps 4-7 the keys, 8-11 the values
@@ -474,17 +502,17 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
     const uint32_t tS0 = tbase + tt * 128 + lane_off, tO = tbase + 256 + tt * 128 + lane_off;
     uint32_t g = 0;
     for (int item = blockIdx.x; item < a.nitems && ok; item += gridDim.x) {
-      const Item it = get_item<KV4>(a, item, &bad);
+      const Item it = get_item<KV4, MASK>(a, item, &bad);
       const int r = it.row0 + tt * kRows + quad * 32 + lane;
       int lim = it.len;
       bool row_live = r < a.R;
       if constexpr (KV4) {
         const int i = r % a.Nq;
         row_live = row_live && i < it.ql;
-        if (a.causal) lim = max(0, it.len - it.ql + i + 1);
+        if constexpr (MASK) lim = max(0, it.len - it.ql + i + 1);
       }
       float m = -INFINITY, l = 0.0f;
-      float ev = -100.0f;  // cache: O holds values times 2^(kPUp + kVUp - ev)
+      float ev = -100.0f;  // cache: O holds values times 2^(kPUp + kVUp - ev); NaN: the row saw one that is not finite
       for (int t = 0; t < it.nb; ++t, ++g) {
         const uint32_t buf = g & 1, tS = tS0 + buf * 64;
         if (!(ok = wait_warp(s_full + tt * 2 + buf, (g >> 1) & 1, abort_flag))) break;
@@ -516,6 +544,10 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
 #pragma unroll
           for (int j = 0; j < kKeys; ++j)
             if (j >= left) s[j] = -INFINITY;
+          if constexpr (MASK) {  // values that the row does not see leave its exponent alone
+            if (left <= 0) e_lo = kUnseen;
+            if (left <= 32) e_hi = kUnseen;
+          }
         }
         float top[4];
 #pragma unroll
@@ -535,7 +567,7 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
           m = mb;
           l *= f;
         }
-        bool turned = up;
+        bool turned = up, odd = false;
         if constexpr (KV4) {
           const float et = fmaxf(e_lo, e_hi);
           if (et > ev) {
@@ -543,10 +575,53 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
             ev = et;
             turned = true;
           }
+          if constexpr (MASK) {
+            odd = fminf(e_lo, e_hi) == kOdd;
+            turned = turned || odd;
+          }
           e_lo = kPUp + fmaxf(e_lo - ev, -64.0f);  // values below 2^-64 of the largest do not count
           e_hi = kPUp + fmaxf(e_hi - ev, -64.0f);
         }
         const bool any_up = __any_sync(0xFFFFFFFFu, turned);
+        if constexpr (MASK) {
+          if (any_up) {
+            if (odd) {
+              float e[2] = {left > 0 ? v_exp[stg * 2] : kUnseen, left > 32 ? v_exp[stg * 2 + 1] : kUnseen};
+              const float was = ev;
+              bool spoiled = false;
+#pragma unroll
+              for (int c = 0; c < 2; ++c) {
+                if (e[c] != kOdd) continue;
+                const int n = min(left - 32 * c, 32);  // keys of these 32 that the row sees, at least one
+                spoiled = spoiled || (v_bad[stg * 2 + c] << (32 - n)) != 0;
+                float et = -100.0f;
+                for (int j = 0; j < n; ++j) et = fmaxf(et, ceilf(v_log[stg * kKeys + 32 * c + j]));
+                if (et > ev) ev = et;
+              }
+              if (ev > was) f *= ex2_approx(was - ev);
+              if (spoiled) ev = NAN;
+              // The sum is taken here; then the scores take the values' scales.
+              const float mr = m == -INFINITY ? 0.0f : m;
+#pragma unroll
+              for (int c = 0; c < 2; ++c) {
+                if (e[c] != kOdd) {
+                  e[c] = kPUp + fmaxf(e[c] - ev, -64.0f);
+                  continue;
+                }
+                e[c] = kNoSum;
+#pragma unroll
+                for (int j = 0; j < 32; ++j) {
+                  l += ex2_approx(s[32 * c + j] - mr);
+                  const float up_v = v_log[stg * kKeys + 32 * c + j] + (kPUp - ev - kNoSum);
+                  s[32 * c + j] = isnan(ev) ? -INFINITY : s[32 * c + j] + up_v;
+                }
+              }
+              e_lo = e[0];
+              e_hi = e[1];
+            }
+            __syncwarp();
+          }
+        }
         if (any_up && t > 0) {  // O holds the blocks before this one
           if (!(ok = wait_warp(pv_done + tt * 2 + (buf ^ 1), ((g - 1) >> 1) & 1, abort_flag))) break;
           tc_fence_after();
@@ -715,11 +790,11 @@ bool make_map(CUtensorMap* m, const void* base, int B, int H, int N, int D, cons
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int D, bool KV4>
+template <int D, bool KV4, bool MASK>
 cudaError_t launch_tiles(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv, const TileArgs& a,
                          cudaStream_t st) {
   using C = CfgT<D, KV4>;
-  auto kern = attn_tiles_kernel<D, KV4>;
+  auto kern = attn_tiles_kernel<D, KV4, MASK>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
   if (e != cudaSuccess) return e;
   return launch_early(kern, dim3(a.nitems < kNumSMs ? a.nitems : kNumSMs), C::kThreads, C::kSmem, st, mq, mk, mv, a);
@@ -744,11 +819,13 @@ cudaError_t launch_kv4_tiles(const ra_kv4_cache& c, const ra_kv4_attn& at, const
   a.kv_lens = seq_lens; a.q_lens = q_lens; a.table = table;
   a.k4 = c.k4; a.sk = c.sk; a.v4 = c.v4; a.sv = c.sv;
   a.num_pages = c.num_pages; a.page_log2 = __builtin_ctz(static_cast<unsigned>(c.page_size));
-  a.max_pages = at.max_pages; a.Nq = at.Nq; a.causal = at.causal;
+  a.max_pages = at.max_pages; a.Nq = at.Nq;
   a.parts = parts;
   CUtensorMap mq;
   if (!make_map(&mq, q, at.B, c.Hk, a.R, c.D, a.os, kRows)) return cudaErrorInvalidValue;
-  return c.D == 64 ? launch_tiles<64, true>(mq, mq, mq, a, st) : launch_tiles<128, true>(mq, mq, mq, a, st);
+  if (at.causal)
+    return c.D == 64 ? launch_tiles<64, true, true>(mq, mq, mq, a, st) : launch_tiles<128, true, true>(mq, mq, mq, a, st);
+  return c.D == 64 ? launch_tiles<64, true, false>(mq, mq, mq, a, st) : launch_tiles<128, true, false>(mq, mq, mq, a, st);
 }
 
 cudaError_t launch_attn_cross(const ra_cross_problem& p, const void* q, const ra_strides& qs, const void* k,
@@ -769,7 +846,7 @@ cudaError_t launch_attn_cross(const ra_cross_problem& p, const void* q, const ra
   if (!make_map(&mq, q, p.B, p.H, p.Nq, p.D, qs, kRows) || !make_map(&mk, k, p.B, p.Hk, p.Nk, p.D, ks, kKeys) ||
       !make_map(&mv, v, p.B, p.Hk, p.Nk, p.D, vs, kKeys))
     return cudaErrorInvalidValue;
-  return p.D == 64 ? launch_tiles<64, false>(mq, mk, mv, a, st) : launch_tiles<128, false>(mq, mk, mv, a, st);
+  return p.D == 64 ? launch_tiles<64, false, false>(mq, mk, mv, a, st) : launch_tiles<128, false, false>(mq, mk, mv, a, st);
 }
 
 cudaError_t read_tiles_status(uint32_t* out) {

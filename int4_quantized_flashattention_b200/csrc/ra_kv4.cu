@@ -65,13 +65,6 @@ __device__ __forceinline__ long long token_row(const CacheArgs& a, int s, int t)
   return ((static_cast<long long>(page) * a.Hk) << a.page_log2) + (pos & ((1 << a.page_log2) - 1));
 }
 
-// The larger one, NaN if either is.
-__device__ __forceinline__ float max_nan(float a, float b) {
-  float d;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
-  return d;
-}
-
 // The largest magnitude among eight bf16, NaN if one of them is.
 __device__ __forceinline__ float max_abs_bf16(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
   auto mag = [](uint32_t w) {

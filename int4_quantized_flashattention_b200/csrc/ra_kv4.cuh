@@ -38,6 +38,13 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   return d;
 }
 
+// The larger one, NaN if either is.
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+  return d;
+}
+
 // (a & b) ^ c
 __device__ __forceinline__ uint32_t and_xor(uint32_t a, uint32_t b, uint32_t c) {
   uint32_t d;

@@ -25,7 +25,8 @@ def gen():
     return torch.Generator(device="cuda").manual_seed(14)
 
 
-SHAPES = [(4, 4, 3, 9), (2, 1, 4, 33), (1, 1, 8, 40), (2, 1, 8, 64), (16, 1, 1, 50), (1, 1, 16, 5000), (1, 1, 16, 16)]
+SHAPES = [(4, 4, 3, 9), (2, 1, 4, 33), (1, 1, 8, 40), (2, 1, 8, 64), (16, 1, 1, 50), (1, 1, 16, 5000), (2, 1, 16, 5000),
+          (1, 1, 16, 16), (2, 1, 40, 70), (1, 1, 100, 100), (1, 1, 300, 4000), (2, 1, 33, 33)]
 
 
 def _inputs(ra, gen, H, Hk, Nq, length, D, spoil):
