@@ -44,6 +44,11 @@ constexpr int kTiles = 2;    // query tiles per CTA
 constexpr int kKeys = 64;    // keys per block = MMA N of S
 // The reference maximum moves when a score passes it by kLazy (powers of two).
 template <bool KV4> constexpr float kLazy = KV4 ? 4.0f : 8.0f;
+// A score is off by about 2^-24 of its size, and x = score - reference, taken in one operation,
+// by half a unit of the reference, which P does not hold from some size on.  From 2^kFar on, a
+// row's differences are halved until the reference is below it: where scores are off by whole
+// powers of two, only what is within their error changes its weight.
+template <bool KV4> constexpr int kFar = KV4 ? 23 : 28;
 constexpr float kPUp = 11.0f;  // cache: P goes to f16 times 2^kPUp, at most 2^15
 constexpr int kVUp = 12;       // and the values times 2^kVUp, at most 7 * 2^12: a scale keeps its bits down to
                                // 2^-26 of the largest of its 32 keys
@@ -51,8 +56,8 @@ constexpr int kVUp = 12;       // and the values times 2^kVUp, at most 7 * 2^12:
 // finite, go to the products as codes, and their scales into P of each row, relative to the
 // largest that the row sees: with one exponent for all rows, keys that a row does not see would
 // take its bits.  A form of the kernel by itself, as what looks for such values costs where
-// there are none (a frame of 1560 rows over 32760 keys, causal and not: 1405 and 1366 us at
-// D = 128, 1396 and 1210 at D = 64).
+// there are none (a frame of 1560 rows over 32760 keys, causal and not: 1455 and 1362 us at
+// D = 128, 1311 and 1236 at D = 64).
 constexpr int kApart = 8;
 constexpr float kOdd = -200.0f, kUnseen = -150.0f;  // in place of an exponent (which is at least -100)
 constexpr float kNoSum = 140.0f;                    // a shift whose inverse, 2^-140, is zero
@@ -64,13 +69,14 @@ struct CfgT {
   static constexpr int kHalf = kKeys * 128;            // and of a K or V block
   static constexpr int kQBytes = kRows * D * 2;
   static constexpr int kKVBytes = kKeys * D * 2;
-  static constexpr int kStages = 4;                    // of K, and of V
+  static constexpr int kStages = KV4 && D == 64 ? 8 : 4;  // of K, and of V (cache at D = 64: as many as there is room
+                                                          // for, 1297 us with four, 1237 with eight)
   static constexpr int oQ = 0;
   static constexpr int oK = oQ + kTiles * kQBytes;
   static constexpr int oV = oK + kStages * kKVBytes;
   static constexpr int oScale = oV + kStages * kKVBytes;      // [sk | log2 sv][stage][key], cache only
   static constexpr int oVExp = oScale + (KV4 ? 2 * kStages * kKeys * 4 : 0);   // [stage][half]: exponents, then masks
-  static constexpr int oStage = oVExp + (KV4 ? 128 : 0);                       // [softmax warp][row][kPiece]
+  static constexpr int oStage = oVExp + (KV4 ? 16 * kStages : 0);              // [softmax warp][row][kPiece]
   static constexpr int kPiece = KV4 ? 64 : 128;        // bytes of a row that leave at a time
   static constexpr int oBar = oStage + 8 * 32 * kPiece;
   static constexpr int kNumBars = 2 + 2 + 5 * kStages + 4 + 4 + 4 + 2;
@@ -358,7 +364,7 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
   } else if (KV4 && warp < C::kFirstSoftmax) {
     // -------------------------------------------------------------- unpacking warps
     if constexpr (C::kTwoUnpack) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
-    else asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    else asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");  // 72 and 192 for the softmax: 1340 us, not 1297
     if constexpr (KV4) {
       constexpr int kQ = D / 64;  // 16-byte pieces of a code row per thread: two threads per key
       const int row = threadIdx.x & 63, part = (threadIdx.x >> 6) & 1;
@@ -494,7 +500,7 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
   } else {
     // -------------------------------------------------------------- softmax, one row per thread
     if constexpr (C::kTwoUnpack) asm volatile("setmaxnreg.inc.sync.aligned.u32 152;");
-    else if constexpr (KV4) asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
+    else if constexpr (KV4) asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
     else asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
     const int tt = (warp - C::kFirstSoftmax) >> 2;
     const int quad = warp & 3;
@@ -512,6 +518,7 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
         if constexpr (MASK) lim = max(0, it.len - it.ql + i + 1);
       }
       float m = -INFINITY, l = 0.0f;
+      float small = 1.0f;  // what differences of scores are multiplied with: 1 below 2^kFar
       float ev = -100.0f;  // cache: O holds values times 2^(kPUp + kVUp - ev); NaN: the row saw one that is not finite
       for (int t = 0; t < it.nb; ++t, ++g) {
         const uint32_t buf = g & 1, tS = tS0 + buf * 64;
@@ -566,6 +573,8 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
         if (up) {
           m = mb;
           l *= f;
+          const int far = static_cast<int>((__float_as_uint(m) >> 23) & 0xFFu) - (126 + kFar<KV4>);
+          small = __uint_as_float((127u - max(far, 0)) << 23);
         }
         bool turned = up, odd = false;
         if constexpr (KV4) {
@@ -601,7 +610,7 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
               if (ev > was) f *= ex2_approx(was - ev);
               if (spoiled) ev = NAN;
               // The sum is taken here; then the scores take the values' scales.
-              const float mr = m == -INFINITY ? 0.0f : m;
+              const float mr = m == -INFINITY ? 0.0f : m, large = 1.0f / small;
 #pragma unroll
               for (int c = 0; c < 2; ++c) {
                 if (e[c] != kOdd) {
@@ -611,8 +620,8 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
                 e[c] = kNoSum;
 #pragma unroll
                 for (int j = 0; j < 32; ++j) {
-                  l += ex2_approx(s[32 * c + j] - mr);
-                  const float up_v = v_log[stg * kKeys + 32 * c + j] + (kPUp - ev - kNoSum);
+                  l += ex2_approx((s[32 * c + j] - mr) * small);
+                  const float up_v = (v_log[stg * kKeys + 32 * c + j] + (kPUp - ev - kNoSum)) * large;
                   s[32 * c + j] = isnan(ev) ? -INFINITY : s[32 * c + j] + up_v;
                 }
               }
@@ -639,8 +648,9 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
             tmem_st_row_nw<32>(tO + c, o);
           }
         }
-        const float mr = m == -INFINITY ? 0.0f : m;
-        const float2 c2 = make_float2(a.scale_log2, a.scale_log2);
+        const float mr = m == -INFINITY ? 0.0f : m * small;
+        const float cr = KV4 ? small : a.scale_log2 * small;
+        const float2 c2 = make_float2(cr, cr);
         float sum = 0.0f;
 #pragma unroll
         for (int c = 0; c < kKeys; c += 32) {
@@ -651,13 +661,8 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
 #pragma unroll
           for (int j = 0; j < 32; j += 4) {
             float2 x = make_float2(s[c + j], s[c + j + 1]), y = make_float2(s[c + j + 2], s[c + j + 3]);
-            if constexpr (KV4) {
-              x = __fadd2_rn(x, m2);
-              y = __fadd2_rn(y, m2);
-            } else {
-              x = __ffma2_rn(x, c2, m2);
-              y = __ffma2_rn(y, c2, m2);
-            }
+            x = __ffma2_rn(x, c2, m2);
+            y = __ffma2_rn(y, c2, m2);
             x = make_float2(ex2_approx(x.x), ex2_approx(x.y));
             y = make_float2(ex2_approx(y.x), ex2_approx(y.y));
             sum2 = __fadd2_rn(sum2, x);

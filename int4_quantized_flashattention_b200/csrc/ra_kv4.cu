@@ -302,7 +302,7 @@ constexpr int kStages = 3;
 // rows: three 8 % faster than two, four 37 % slower; 225 us).
 template <int D, int NT> constexpr int kRowsPerSm = NT == 2 ? 3 : D == 128 ? 4 : 5;
 constexpr float kLazy = 4.0f;  // the reference maximum moves when a score passes it by this (powers of two)
-constexpr float kNone = -1e30f;  // reference of a row that has met no key: finite, so that -inf - kNone is -inf
+constexpr float kNone = -3e38f;  // reference of a row that has met no key: finite, so that -inf - kNone is -inf
 constexpr float kPUp = 2048.0f;  // P goes to f16 times this: at most 2^(4 + 11), below 2^-25 it loses bits
 constexpr uint32_t kPUpBits = (127u + 127 + 11) << 23;  // less the bits of a power of two: those of kPUp over it
 
@@ -542,7 +542,8 @@ __global__ void __launch_bounds__(kRowWarps * 32, kRowsPerSm<D, NT>) kv4_rows_ke
           float x = kNone;
 #pragma unroll
           for (int u = 0; u < 2; ++u)
-            x = fmaxf(x, fmaxf(s[j][u][n] * (fk[u][0] * q_down[j][n]), s[j][u][2 + n] * (fk[u][1] * q_down[j][n])));
+            x = fmaxf(x, fmaxf(__fmul_rn(s[j][u][n], fk[u][0] * q_down[j][n]),
+                               __fmul_rn(s[j][u][2 + n], fk[u][1] * q_down[j][n])));
 #pragma unroll
           for (int o = 4; o < 32; o <<= 1) x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, o));
           const float mn = fmaxf(m[j][n], x);
@@ -571,7 +572,8 @@ __global__ void __launch_bounds__(kRowWarps * 32, kRowsPerSm<D, NT>) kv4_rows_ke
 #pragma unroll
           for (int e = 0; e < 2; ++e)
 #pragma unroll
-            for (int n = 0; n < 2; ++n) z[j][u][2 * e + n] = fmaf(s[j][u][2 * e + n], fk[u][e] * q_down[j][n], -m[j][n]);
+            for (int n = 0; n < 2; ++n)  // the product rounded as in the maximum: scores of 2^27 and more are off by powers
+              z[j][u][2 * e + n] = __fmul_rn(s[j][u][2 * e + n], fk[u][e] * q_down[j][n]) - m[j][n];
 #pragma unroll
         for (int i = 0; i < kM; ++i) {
           acc[j][i][0] *= f[0];
