@@ -476,7 +476,8 @@ typedef struct {
 
 /*
  *   q [B, H, Nq, D], k, v [B, Hk, Nk, D], out [B, H, Nq, D]: bf16 with strides;
- *               out's are at least D, and out overlaps no input.
+ *               out's rows lie clear of one another (each axis steps over all
+ *               that the axes of smaller strides span), and of the inputs.
  *   kv_lens     [B] int32: keys of each batch entry; key and value rows behind
  *               them take no part, whatever they hold (NaN too).  NULL: all Nk.
  *               Lengths outside [0, Nk] are reported by ra_sync_status and

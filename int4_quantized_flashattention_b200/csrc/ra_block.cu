@@ -4,6 +4,7 @@
 
 #include <cmath>
 #include <cstdint>
+#include <utility>
 
 #include "ra_block.h"
 #include "ra_internal.h"
@@ -26,6 +27,26 @@ bool valid_strides(const ra_strides* s, int B, int H, int N, int size) {
   const int ext[3] = {B, H, N};
   for (int i = 0; i < 3; ++i)
     if (ext[i] > 1 && (st[i] < 1 || st[i] >= kMaxStride || (st[i] * size) % 16 != 0)) return false;
+  return true;
+}
+
+// Rows of D elements that lie clear of one another: of the axes with more than one entry,
+// each steps over all that the ones of smaller strides span.
+bool rows_apart(const ra_strides& s, int B, int H, int N, int D) {
+  int64_t st[3] = {s.b, s.h, s.n};
+  int ext[3] = {B, H, N};
+  for (int i = 0; i < 2; ++i)
+    for (int j = 0; j < 2; ++j)
+      if (st[j] > st[j + 1]) {
+        std::swap(st[j], st[j + 1]);
+        std::swap(ext[j], ext[j + 1]);
+      }
+  int64_t span = D;
+  for (int i = 0; i < 3; ++i) {
+    if (ext[i] == 1) continue;
+    if (st[i] < span || ext[i] - 1 > (1LL << 46) / st[i]) return false;  // 2^46 elements: no memory holds them
+    span += (ext[i] - 1) * st[i];
+  }
   return true;
 }
 
@@ -173,9 +194,7 @@ ra_status ra_attn_cross(const ra_cross_problem* p, const void* q, const ra_strid
   if (!valid_strides(q_st, p->B, p->H, p->Nq, 2) || !valid_strides(k_st, p->B, p->Hk, p->Nk, 2) ||
       !valid_strides(v_st, p->B, p->Hk, p->Nk, 2) || !valid_strides(out_st, p->B, p->H, p->Nq, 2))
     return RA_ERR_INVALID_ARG;
-  // Rows of the output must not lie over one another.
-  if ((p->B > 1 && out_st->b < p->D) || (p->H > 1 && out_st->h < p->D) || (p->Nq > 1 && out_st->n < p->D))
-    return RA_ERR_INVALID_ARG;
+  if (!rows_apart(*out_st, p->B, p->H, p->Nq, p->D)) return RA_ERR_INVALID_ARG;
   return from_cuda(ra::launch_attn_cross(*p, q, *q_st, k, *k_st, v, *v_st, kv_lens, out, *out_st, lse,
                                          static_cast<cudaStream_t>(stream)));
 }
