@@ -20,6 +20,9 @@ ra_status from_cuda(cudaError_t e) { return e == cudaSuccess ? RA_OK : RA_ERR_CU
 constexpr int kMaxGrid = 65535;          // CUDA's limit on grid y and z
 constexpr int64_t kMaxStride = 1LL << 38;  // elements; a tensor map's byte strides end at 2^40
 
+// a * b < limit for positive values whose product may not fit 64 bits.
+bool below(int64_t a, int64_t b, int64_t limit) { return a < limit && b < limit && a * b < limit; }
+
 // Strides of a [B, H, N, D] tensor with elements of `size` bytes.
 bool valid_strides(const ra_strides* s, int B, int H, int N, int size) {
   if (!s) return false;
@@ -54,9 +57,9 @@ bool valid_dim(int D) { return D == 64 || D == 128; }
 
 bool valid_cache(const ra_kv4_cache* c) {
   if (!c || c->num_pages < 1 || c->Hk < 1 || c->Hk > kMaxGrid / 2 || !valid_dim(c->D)) return false;
+  if (c->page_size != 16 && c->page_size != 32 && c->page_size != 64 && c->page_size != 128) return false;
   // The kernels count the cache's rows in 32 bits (2^32 of them are more than the memory holds).
   if (static_cast<int64_t>(c->num_pages) * c->Hk * c->page_size > (1LL << 32) - 1) return false;
-  if (c->page_size != 16 && c->page_size != 32 && c->page_size != 64 && c->page_size != 128) return false;
   return aligned16(c->k4) && aligned16(c->sk) && aligned16(c->v4) && aligned16(c->sv);
 }
 
@@ -71,7 +74,7 @@ bool valid_kv4_attn(const ra_kv4_cache* c, const ra_kv4_attn* a) {
   if (!c || !a || c->Hk < 1 || !valid_dim(c->D)) return false;
   if (a->B < 1 || a->H < 1 || a->Nq < 1 || a->max_len < 0 || a->H % c->Hk != 0) return false;
   if (!(a->scale > 0.0f) || !std::isfinite(a->scale) || (a->causal != 0 && a->causal != 1)) return false;
-  return static_cast<int64_t>(a->B) * a->H * a->Nq * c->D < (1LL << 31);
+  return below(static_cast<int64_t>(a->B) * a->H, a->Nq, (1LL << 31) / c->D);
 }
 
 }  // namespace
@@ -187,7 +190,7 @@ ra_status ra_attn_cross(const ra_cross_problem* p, const void* q, const ra_strid
     return RA_ERR_INVALID_ARG;
   if (p->Nq > (1 << 24) || p->Nk > (1 << 24) || !(p->scale > 0.0f) || !std::isfinite(p->scale))
     return RA_ERR_INVALID_ARG;
-  if (static_cast<int64_t>(p->B) * p->H * ((p->Nq + 255) / 256) >= (1LL << 30)) return RA_ERR_INVALID_ARG;
+  if (!below(static_cast<int64_t>(p->B) * p->H, (p->Nq + 255) / 256, 1LL << 30)) return RA_ERR_INVALID_ARG;
   if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(out) || !aligned4_or_null(lse) ||
       !aligned4_or_null(kv_lens))
     return RA_ERR_INVALID_ARG;
