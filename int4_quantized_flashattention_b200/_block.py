@@ -126,14 +126,20 @@ def qk_norm_rope(p: Problem, q: Optional[torch.Tensor], k: Optional[torch.Tensor
 
 class KV4Cache:
     """A paged 4-bit key/value cache (ra_kv4_cache): codes k4, v4 [num_pages, Hk, page_size, D/2] uint8 and scales
-    sk, sv [num_pages, Hk, page_size] fp32.  Only a handle: the tensors are the caller's, kept alive by it."""
+    sk, sv [num_pages, Hk, page_size] fp32.  Only a handle: the tensors are the caller's, kept alive by it.  They
+    cannot be exchanged for others, and every call looks at them as they then are."""
 
-    __slots__ = ("k4", "sk", "v4", "sv", "index", "_c")
+    __slots__ = ("_tensors", "_index")
 
     def __init__(self, k4: torch.Tensor, sk: torch.Tensor, v4: torch.Tensor, sv: torch.Tensor):
-        self._c = (_ext or _bind()).kv4_cache(k4, sk, v4, sv)
-        self.k4, self.sk, self.v4, self.sv, self.index = k4, sk, v4, sv, k4.get_device()
+        (_ext or _bind()).kv4_cache(k4, sk, v4, sv)  # checks them
+        self._tensors, self._index = (k4, sk, v4, sv), k4.get_device()
 
+    k4 = property(lambda self: self._tensors[0])
+    sk = property(lambda self: self._tensors[1])
+    v4 = property(lambda self: self._tensors[2])
+    sv = property(lambda self: self._tensors[3])
+    index = property(lambda self: self._index, doc="Index of the CUDA device.")
     num_pages = property(lambda self: self.k4.shape[0])
     Hk = property(lambda self: self.k4.shape[1])
     page_size = property(lambda self: self.k4.shape[2])
@@ -155,8 +161,9 @@ def kv4_append(cache: KV4Cache, k: torch.Tensor, v: torch.Tensor, block_table: t
     """ra_kv4_append: quantises k, v [B, Hk, T, D] (any strides with contiguous channels) into the cache at
     positions start[b] + 0 .. n_new[b] - 1 of each sequence."""
     if stream is not None:
-        return _run("kv4_append", cache.index, stream, cache._c, cache.index, k, v, block_table, start, n_new)
-    return (_ext or _bind()).kv4_append(cache._c, cache.index, k, v, block_table, start, n_new)
+        return _run("kv4_append", cache._index, stream, cache._tensors, cache._index, k, v, block_table, start,
+                    n_new)
+    return (_ext or _bind()).kv4_append(cache._tensors, cache._index, k, v, block_table, start, n_new)
 
 
 def kv4_read(cache: KV4Cache, block_table: torch.Tensor, start: Optional[torch.Tensor], T: int,
@@ -169,16 +176,16 @@ def kv4_read(cache: KV4Cache, block_table: torch.Tensor, start: Optional[torch.T
     k, v = (None, None) if out is None else out
     if (k is None) != (v is None):
         raise ValueError("out must hold both tensors")
-    args = (cache._c, cache.index, block_table, start, T, n, dtype is _F32, k, v)
+    args = (cache._tensors, cache._index, block_table, start, T, n, dtype is _F32, k, v)
     if stream is not None:
-        return _run("kv4_read", cache.index, stream, *args)
+        return _run("kv4_read", cache._index, stream, *args)
     return (_ext or _bind()).kv4_read(*args)
 
 
 def attn_kv4_workspace_bytes(cache: KV4Cache, B: int, H: int, Nq: int, max_len: int) -> int:
     """Bytes of workspace attn_kv4 needs for queries [B, H, Nq, D] and sequences of up to max_len keys."""
     a = _Kv4Attn(B, H, Nq, 1, max_len, 0, 1.0)
-    return int(lib().ra_attn_kv4_workspace_bytes(cache._c, C.byref(a)))
+    return int(lib().ra_attn_kv4_workspace_bytes(_bind().kv4_cache(*cache._tensors), C.byref(a)))
 
 
 def attn_kv4(cache: KV4Cache, q: torch.Tensor, block_table: torch.Tensor, seq_lens: torch.Tensor,
@@ -187,9 +194,9 @@ def attn_kv4(cache: KV4Cache, q: torch.Tensor, block_table: torch.Tensor, seq_le
              workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """ra_attn_kv4: attention of q [B, H, Nq, D] bf16 over the cache; returns out [B, H, Nq, D] bf16.  max_len is a
     bound on seq_lens that the split of the keys is planned for (the block table's reach by default)."""
-    args = (cache._c, cache.index, q, block_table, seq_lens, q_lens, causal, scale, max_len, out, lse, workspace)
+    args = (cache._tensors, cache._index, q, block_table, seq_lens, q_lens, causal, scale, max_len, out, lse, workspace)
     if stream is not None:
-        return _run("attn_kv4", cache.index, stream, *args)
+        return _run("attn_kv4", cache._index, stream, *args)
     return (_ext or _bind()).attn_kv4(*args)
 
 

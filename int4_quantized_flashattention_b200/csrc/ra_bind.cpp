@@ -266,22 +266,39 @@ PyObject* qk_norm_rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
+// The cache that four tensors hold now.
+ra_kv4_cache cache_of(PyObject* const* a) {
+  const at::Tensor& k4 = cuda4(a[0], "k4");
+  const c10::IntArrayRef codes = k4.sizes(), scales = codes.slice(0, 3);
+  const c10::Device dev = k4.device();
+  ra_kv4_cache c;
+  std::memset(&c, 0, sizeof(c));
+  c.num_pages = extent(codes[0]);
+  c.Hk = extent(codes[1]);
+  c.page_size = extent(codes[2]);
+  c.D = extent(2 * codes[3]);
+  c.k4 = static_cast<uint8_t*>(arg(a[0], "k4", at::kByte, codes, dev));
+  c.sk = static_cast<float*>(arg(a[1], "sk", at::kFloat, scales, dev));
+  c.v4 = static_cast<uint8_t*>(arg(a[2], "v4", at::kByte, codes, dev));
+  c.sv = static_cast<float*>(arg(a[3], "sv", at::kFloat, scales, dev));
+  return c;
+}
+
+// A cache as a tuple of its tensors (k4, sk, v4, sv) on `dev`, or as the bytes that kv4_cache made of them.  Tensors
+// are looked at in every call: memory that they were moved to or from since the last one is not mistaken for theirs.
+ra_kv4_cache cache_arg(PyObject* o, c10::Device dev) {
+  if (!PyTuple_Check(o)) return structure<ra_kv4_cache>(o, "cache");
+  if (PyTuple_GET_SIZE(o) != 4) value_error("cache is not the four tensors expected");
+  PyObject* const t[4] = {PyTuple_GET_ITEM(o, 0), PyTuple_GET_ITEM(o, 1), PyTuple_GET_ITEM(o, 2), PyTuple_GET_ITEM(o, 3)};
+  const ra_kv4_cache c = cache_of(t);
+  if (THPVariable_Unpack(t[0]).device() != dev) value_error("the cache's tensors have left " + dev.str());
+  return c;
+}
+
 // k4, sk, v4, sv -> the ra_kv4_cache as bytes
 PyObject* kv4_cache(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return entry(n, 4, [&]() -> PyObject* {
-    const at::Tensor& k4 = cuda4(a[0], "k4");
-    const c10::IntArrayRef codes = k4.sizes(), scales = codes.slice(0, 3);
-    const c10::Device dev = k4.device();
-    ra_kv4_cache c;
-    std::memset(&c, 0, sizeof(c));
-    c.num_pages = extent(codes[0]);
-    c.Hk = extent(codes[1]);
-    c.page_size = extent(codes[2]);
-    c.D = extent(2 * codes[3]);
-    c.k4 = static_cast<uint8_t*>(arg(a[0], "k4", at::kByte, codes, dev));
-    c.sk = static_cast<float*>(arg(a[1], "sk", at::kFloat, scales, dev));
-    c.v4 = static_cast<uint8_t*>(arg(a[2], "v4", at::kByte, codes, dev));
-    c.sv = static_cast<float*>(arg(a[3], "sv", at::kFloat, scales, dev));
+    const ra_kv4_cache c = cache_of(a);
     return PyBytes_FromStringAndSize(reinterpret_cast<const char*>(&c), sizeof(c));
   });
 }
@@ -306,8 +323,8 @@ c10::Device device(PyObject* index) {
 // cache, device index, k, v, block_table, start, n_new
 PyObject* kv4_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return entry(n, 7, [&]() -> PyObject* {
-    const ra_kv4_cache c = structure<ra_kv4_cache>(a[0], "cache");
     const c10::Device dev = device(a[1]);
+    const ra_kv4_cache c = cache_arg(a[0], dev);
     const c10::cuda::OptionalCUDAGuard guard(dev);
     const at::Tensor& k = cuda4(a[2], "k");
     const at::Tensor& v = cuda4(a[3], "v");
@@ -329,8 +346,8 @@ PyObject* kv4_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
 // cache, device index, block_table, start, T, n, fp32 (truth value), k, v (outputs or None)
 PyObject* kv4_read(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return entry(n, 9, [&]() -> PyObject* {
-    const ra_kv4_cache c = structure<ra_kv4_cache>(a[0], "cache");
     const c10::Device dev = device(a[1]);
+    const ra_kv4_cache c = cache_arg(a[0], dev);
     const c10::cuda::OptionalCUDAGuard guard(dev);
     const at::Tensor& t = tensor(a[2], "block_table");
     const int64_t B = t.dim() > 0 ? t.size(0) : 0;
@@ -354,8 +371,8 @@ PyObject* kv4_read(PyObject*, PyObject* const* a, Py_ssize_t n) {
 // cache, device index, q, block_table, seq_lens, q_lens, causal, scale, max_len, out, lse, workspace
 PyObject* attn_kv4(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return entry(n, 12, [&]() -> PyObject* {
-    const ra_kv4_cache c = structure<ra_kv4_cache>(a[0], "cache");
     const c10::Device dev = device(a[1]);
+    const ra_kv4_cache c = cache_arg(a[0], dev);
     const c10::cuda::OptionalCUDAGuard guard(dev);
     const at::Tensor& q = cuda4(a[2], "q");
     const c10::IntArrayRef shape = q.sizes();
