@@ -5,6 +5,7 @@ import os
 import subprocess
 import sys
 import sysconfig
+import warnings
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(PKG, "csrc")
@@ -46,25 +47,43 @@ def build(force: bool = False, verbose: bool = False) -> str:
         tmp = LIB + ".tmp"
         subprocess.run(["nvcc"] + ARCH + ["-shared", "-cudart", "static", "-o", tmp] + objs, check=True)
         os.replace(tmp, LIB)
-    build_bind(force)
+    try:
+        build_bind(force)
+    except (OSError, subprocess.CalledProcessError) as e:
+        # libra.so and what is bound by ctypes do not need it; the operators that do say so when they are called.
+        warnings.warn(f"the compiled binding could not be built ({e}): the operators around the attention will not "
+                      "be available", RuntimeWarning)
     return LIB
 
 
 def build_bind(force: bool = False) -> str:
-    """Compiles the binding against the installed torch and libra.so beside it."""
+    """Compiles the binding against the installed torch and libra.so beside it; anew for another torch or Python."""
     import torch
     src = os.path.join(CSRC, "ra_bind.cpp")
-    if not force and not _newer(BIND, [src, os.path.join(os.path.dirname(PKG), "include", "ra.h")]):
+    made_for = f"{torch.__version__} {os.path.dirname(torch.__file__)} {sys.version}"
+    stamp = os.path.join(OBJDIR, "bind.txt")
+    same = False
+    if os.path.exists(stamp):
+        with open(stamp) as f:
+            same = f.read() == made_for
+    if not force and same and not _newer(BIND, [src, os.path.join(os.path.dirname(PKG), "include", "ra.h")]):
         return BIND
     root = os.path.dirname(torch.__file__)
     cuda = os.environ.get("CUDA_HOME", "/usr/local/cuda")
     inc = [sysconfig.get_paths()["include"], os.path.join(root, "include"),
            os.path.join(root, "include", "torch", "csrc", "api", "include"), os.path.join(cuda, "include")]
     tmp = BIND + ".tmp"
-    subprocess.run(["g++", "-O2", "-std=c++20", "-shared", "-fPIC"] + [a for i in inc for a in ("-isystem", i)]
-                   + [src, "-o", tmp, "-L" + os.path.join(root, "lib"), "-ltorch_python", "-ltorch_cuda", "-ltorch_cpu",
-                      "-lc10_cuda", "-lc10", "-L" + PKG, "-l:libra.so", "-Wl,-rpath,$ORIGIN"], check=True)
+    try:
+        subprocess.run(["g++", "-O2", "-std=c++20", "-shared", "-fPIC"] + [a for i in inc for a in ("-isystem", i)]
+                       + [src, "-o", tmp, "-L" + os.path.join(root, "lib"), "-ltorch_python", "-ltorch_cuda", "-ltorch_cpu",
+                          "-lc10_cuda", "-lc10", "-L" + PKG, "-l:libra.so", "-Wl,-rpath,$ORIGIN"], check=True)
+    except (OSError, subprocess.CalledProcessError):
+        if os.path.exists(BIND):
+            os.remove(BIND)   # rather none than one that does not fit
+        raise
     os.replace(tmp, BIND)
+    with open(stamp, "w") as f:
+        f.write(made_for)
     return BIND
 
 
