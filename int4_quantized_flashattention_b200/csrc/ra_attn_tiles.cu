@@ -27,6 +27,7 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cstdint>
 
 #include "ra_common.cuh"
@@ -38,6 +39,7 @@ namespace ra {
 namespace {
 
 __device__ uint32_t g_tiles_status = 0;
+std::atomic<bool> g_used{false};  // a program that has never called these does not read their status
 
 constexpr int kRows = 128;   // query rows per tile = MMA M
 constexpr int kTiles = 2;    // query tiles per CTA
@@ -810,6 +812,7 @@ cudaError_t launch_tiles(const CUtensorMap& mq, const CUtensorMap& mk, const CUt
 cudaError_t launch_kv4_tiles(const ra_kv4_cache& c, const ra_kv4_attn& at, const Kv4Plan& plan, const void* q,
                              const int32_t* table, const int32_t* seq_lens, const int32_t* q_lens,
                              const Kv4Parts& parts, void* out, float* lse, cudaStream_t st) {
+  g_used.store(true, std::memory_order_relaxed);
   TileArgs a{};
   a.heads = c.Hk; a.group = 1; a.R = at.H / c.Hk * at.Nq;
   a.npairs = (a.R + kTiles * kRows - 1) / (kTiles * kRows);
@@ -836,6 +839,7 @@ cudaError_t launch_kv4_tiles(const ra_kv4_cache& c, const ra_kv4_attn& at, const
 cudaError_t launch_attn_cross(const ra_cross_problem& p, const void* q, const ra_strides& qs, const void* k,
                               const ra_strides& ks, const void* v, const ra_strides& vs, const int32_t* kv_lens,
                               void* out, const ra_strides& os, float* lse, cudaStream_t st) {
+  g_used.store(true, std::memory_order_relaxed);
   TileArgs a{};
   a.heads = p.H; a.group = p.H / p.Hk; a.R = p.Nq;
   a.npairs = (a.R + kTiles * kRows - 1) / (kTiles * kRows);
@@ -855,6 +859,8 @@ cudaError_t launch_attn_cross(const ra_cross_problem& p, const void* q, const ra
 }
 
 cudaError_t read_tiles_status(uint32_t* out) {
+  *out = 0;
+  if (!g_used.load(std::memory_order_relaxed)) return cudaSuccess;
   uint32_t zero = 0;
   cudaError_t e = cudaMemcpyFromSymbol(out, g_tiles_status, sizeof(uint32_t));
   if (e != cudaSuccess) return e;

@@ -5,6 +5,7 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cstdint>
 
 #include "ra_common.cuh"
@@ -16,6 +17,7 @@ namespace ra {
 namespace {
 
 __device__ uint32_t g_kv4_status = 0;
+std::atomic<bool> g_used{false};  // a program that has never called these does not read their status
 
 constexpr int kThreads = 256;
 // CTAs at once on an SM (4680 tokens x 40 heads, append and read together: 65.4 us with
@@ -795,6 +797,7 @@ CacheKernel read_kernel(int tokens) {
 cudaError_t launch_kv4_append(const ra_kv4_cache& c, int dtype, int B, int T, const void* k, const ra_strides& ks,
                               const void* v, const ra_strides& vs, const int32_t* table, int max_pages,
                               const int32_t* start, const int32_t* n_new, cudaStream_t st) {
+  g_used.store(true, std::memory_order_relaxed);
   dim3 grid;
   const int tokens = tokens_per_thread(c.Hk, append_ahead(dtype == RA_DT_BF16));
   CacheArgs a = cache_args(c, B, T, table, max_pages, start, n_new, c.D / 8, kAppendPerSm,
@@ -808,6 +811,7 @@ cudaError_t launch_kv4_append(const ra_kv4_cache& c, int dtype, int B, int T, co
 
 cudaError_t launch_kv4_read(const ra_kv4_cache& c, int dtype, int B, int T, const int32_t* table, int max_pages,
                             const int32_t* start, const int32_t* n, void* k, void* v, cudaStream_t st) {
+  g_used.store(true, std::memory_order_relaxed);
   dim3 grid;
   const int tokens = tokens_per_thread(c.Hk, kReadAhead);
   CacheArgs a = cache_args(c, B, T, table, max_pages, start, n, dtype == RA_DT_BF16 ? c.D / 8 : c.D / 4,
@@ -857,6 +861,7 @@ Kv4Parts kv4_parts(const ra_kv4_cache& c, const ra_kv4_attn& a, const Kv4Plan& p
 cudaError_t launch_kv4_rows(const ra_kv4_cache& c, const ra_kv4_attn& at, const Kv4Plan& plan, const void* q,
                             const int32_t* table, const int32_t* seq_lens, const int32_t* q_lens,
                             const Kv4Parts& parts, void* out, float* lse, cudaStream_t st) {
+  g_used.store(true, std::memory_order_relaxed);
   RowsArgs a{};
   a.k4 = c.k4; a.sk = c.sk; a.v4 = c.v4; a.sv = c.sv;
   a.q = static_cast<const __nv_bfloat16*>(q);
@@ -884,6 +889,8 @@ cudaError_t launch_kv4_join(const ra_kv4_cache& c, const ra_kv4_attn& a, const K
 }
 
 cudaError_t read_kv4_status(uint32_t* out) {
+  *out = 0;
+  if (!g_used.load(std::memory_order_relaxed)) return cudaSuccess;
   uint32_t zero = 0;
   cudaError_t e = cudaMemcpyFromSymbol(out, g_kv4_status, sizeof(uint32_t));
   if (e != cudaSuccess) return e;

@@ -16,6 +16,7 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cstdint>
 
 #include "ra_common.cuh"
@@ -26,6 +27,7 @@ namespace ra {
 namespace {
 
 __device__ uint32_t g_norm_status = 0;
+std::atomic<bool> g_used{false};  // a program that has never called these does not read their status
 
 constexpr int kThreads = 256;
 // Heads whose loads travel while as many are worked on.
@@ -188,6 +190,7 @@ cudaError_t launch_rot(const NormArgs& a, int rot, bool layer, dim3 grid, cudaSt
 }  // namespace
 
 cudaError_t launch_norm_rope(const ra_problem& p, const NormRopeCall& c, cudaStream_t st) {
+  g_used.store(true, std::memory_order_relaxed);
   NormArgs a{};
   for (int i = 0; i < 2; ++i) {
     a.x[i] = c.x[i];
@@ -218,6 +221,8 @@ cudaError_t launch_norm_rope(const ra_problem& p, const NormRopeCall& c, cudaStr
 }
 
 cudaError_t read_norm_rope_status(uint32_t* out) {
+  *out = 0;
+  if (!g_used.load(std::memory_order_relaxed)) return cudaSuccess;
   uint32_t zero = 0;
   cudaError_t e = cudaMemcpyFromSymbol(out, g_norm_status, sizeof(uint32_t));
   if (e != cudaSuccess) return e;
