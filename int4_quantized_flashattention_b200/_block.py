@@ -100,6 +100,8 @@ def rope_table(p: Problem, device="cuda", stream=None) -> torch.Tensor:
     n = int(lib().ra_rope_table_bytes(C.byref(p)))
     if n == 0:
         raise ValueError("invalid problem")
+    if torch.device(device).type != "cuda":
+        raise ValueError("device must be a CUDA device")
     idx = torch.empty(0, device=device).get_device()
     with _on(idx, stream):
         t = torch.empty(n // 8, 2, dtype=_F32, device="cuda")
