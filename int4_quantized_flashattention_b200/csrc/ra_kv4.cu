@@ -252,7 +252,7 @@ __global__ void __launch_bounds__(kThreads, kReadPerSm) kv4_read_kernel(const Ca
 }
 
 // ---------------------------------------------------------------- attention, few rows
-// A CTA takes up to 8 * NT query rows of one key head and one part of its
+// A CTA takes the query rows of one key head, at most 8 * NT, and one part of its
 // keys; its four warps take 32-key steps in turn, each with its own running
 // maximum, sum and output, joined at the end.  Bound: HBM, the codes and
 // scales of the keys read once ((D + 8) bytes a key and head).
@@ -299,10 +299,10 @@ struct RowsArgs {
 constexpr int kRowWarps = 4;
 constexpr int kStep = 32;    // keys per warp and step
 constexpr int kStages = 3;
-// CTAs at once on an SM, as many as the registers allow; at D = 128 and 9 to 16 rows one
-// more than they would by themselves, for a few spilled (16 x 40 heads x 8191 keys, 16
-// rows: three 8 % faster than two, four 37 % slower; 225 us).
-template <int D, int NT> constexpr int kRowsPerSm = NT == 2 ? 3 : D == 128 ? 4 : 5;
+// CTAs at once on an SM, as many as the registers allow without spilling (16 x 40 heads x 8191
+// keys: D = 128, one row: 3, 4 and 5 take 147, 146 and 162 us, 16 rows: 2, 3 and 4 take 228, 235
+// and 428; D = 64, one row: 4, 5 and 6 take 95, 98 and 100, 16 rows: 2, 3 and 4 take 152, 135 and 141).
+template <int D, int NT> constexpr int kRowsPerSm = NT == 1 ? 4 : D == 128 ? 2 : 3;
 constexpr float kLazy = 4.0f;  // the reference maximum moves when a score passes it by this (powers of two)
 constexpr float kNone = -3e38f;  // reference of a row that has met no key: finite, so that -inf - kNone is -inf
 constexpr float kPUp = 2048.0f;  // P goes to f16 times this: at most 2^(4 + 11), below 2^-25 it loses bits
@@ -334,7 +334,7 @@ __global__ void __launch_bounds__(kRowWarps * 32, kRowsPerSm<D, NT>) kv4_rows_ke
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, q4 = lane & 3;
   const int bh = blockIdx.x, b = bh / a.Hk, hk = bh % a.Hk;
-  const int split = blockIdx.y, r0 = blockIdx.z * 8 * NT;
+  const int split = blockIdx.y;
   const int R = a.G * a.Nq;
   uint32_t bad = 0;
   grid_wait();
@@ -399,7 +399,7 @@ __global__ void __launch_bounds__(kRowWarps * 32, kRowsPerSm<D, NT>) kv4_rows_ke
 #pragma unroll
   for (int j = 0; j < NT; ++j) {
     most[j] = 0.0f;
-    const int r = r0 + 8 * j + g;
+    const int r = 8 * j + g;
     const bool in_use = r < R && r % a.Nq < ql;
     const __nv_bfloat16* const src = a.q + (static_cast<size_t>(bh) * R + (in_use ? r : 0)) * D + q4 * (D / 4);
 #pragma unroll
@@ -439,7 +439,7 @@ __global__ void __launch_bounds__(kRowWarps * 32, kRowsPerSm<D, NT>) kv4_rows_ke
     }
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
-      const int rr = r0 + 8 * j + 2 * q4 + e, i = rr % a.Nq;
+      const int rr = 8 * j + 2 * q4 + e, i = rr % a.Nq;
       lim[j][e] = rr < R && i < ql ? (a.causal ? max(len - ql + i + 1, 0) : len) : 0;
     }
   }
@@ -564,7 +564,7 @@ __global__ void __launch_bounds__(kRowWarps * 32, kRowsPerSm<D, NT>) kv4_rows_ke
           for (int o = 4; o < 32; o <<= 1) v = max(v, __shfl_xor_sync(0xFFFFFFFFu, v, o));
           const bool spoiled = v >= 0x7F800000u;
           const uint32_t was = kPUpBits - __float_as_uint(vinv[j][n]);  // powers of two: differences of bits
-          const uint32_t now = spoiled ? was : max(was, (v + 0x007FFFFFu) & 0x7F800000u);
+          const uint32_t now = spoiled ? was : max(was, min((v + 0x007FFFFFu) & 0x7F800000u, 0x7F000000u));
           vinv[j][n] = __uint_as_float(kPUpBits - now);
           vlim = fminf(vlim, __uint_as_float(now));
           f[n] *= spoiled ? NAN : __uint_as_float(was) * __uint_as_float(0x7F000000u - now);
@@ -665,8 +665,7 @@ __global__ void __launch_bounds__(kRowWarps * 32, kRowsPerSm<D, NT>) kv4_rows_ke
   __syncthreads();
   for (int idx = threadIdx.x; idx < kRows * (D / 4); idx += kRowWarps * 32) {
     const int row = idx / (D / 4), c = (idx % (D / 4)) * 4;
-    const int r = r0 + row;
-    if (r >= R || r % a.Nq >= ql) continue;
+    if (row >= R || row % a.Nq >= ql) continue;
     float top = kNone;
 #pragma unroll
     for (int w = 0; w < kRowWarps; ++w) top = fmaxf(top, rm[w * kRows + row]);
@@ -683,11 +682,11 @@ __global__ void __launch_bounds__(kRowWarps * 32, kRowsPerSm<D, NT>) kv4_rows_ke
     // Sums tell rows without keys (zero) from rows that are not finite (NaN).  Scores of minus
     // infinity alone, 0 / 0, leave a sum of zero too: such a row, or such a part of it, is NaN
     // with a log-sum-exp of -inf, which the join takes for NaN if the row has nothing else.
-    const int i = r % a.Nq;
+    const int i = row % a.Nq;
     const bool sees = t0 < t1 && (a.causal ? len - ql + i + 1 : len) > t0 * kStep;
     const float inv = sum != 0.0f ? 1.0f / sum : sees ? NAN : 0.0f;
     const float lse2 = sum != 0.0f ? top + log2f(sum) : -INFINITY;
-    const size_t at = static_cast<size_t>(bh) * R + r;
+    const size_t at = static_cast<size_t>(bh) * R + row;
     o.x *= inv; o.y *= inv; o.z *= inv; o.w *= inv;
     if (a.nsplit == 1) {
       *reinterpret_cast<uint2*>(a.out + at * D + c) = make_uint2(pack_bf16(o.x, o.y), pack_bf16(o.z, o.w));
@@ -825,13 +824,19 @@ cudaError_t launch_kv4_read(const ra_kv4_cache& c, int dtype, int B, int T, cons
 Kv4Plan kv4_plan(const ra_kv4_cache& c, const ra_kv4_attn& a) {
   Kv4Plan plan{};
   const long long R = static_cast<long long>(a.H / c.Hk) * a.Nq, bh = static_cast<long long>(a.B) * c.Hk;
+  // Up to 16 rows, which one CTA of the few-row kernel holds, that kernel; the tiles take the
+  // same time for 1 row as for 128.  (640 heads x 8191 keys, D = 128: 146, 147, 150, 235 us at
+  // 1, 4, 8, 16 rows against 790 to 800 in tiles, which take 800, 816, 840, 889 at 17, 32, 64,
+  // 128; D = 64: 95 to 133 against 722.  8 heads x 32760 keys: 22 to 30 against 53.  4 x 8 heads x
+  // 700 keys: 8 to 13 against 14.  Several CTAs of 16 rows for 17 to 48 rows, each reading the
+  // keys by itself, measured 400 to 607 us, 46 to 48 and 13, which a later form could take up.)
   plan.tiles = R > 16;
   // The number of parts with the least estimated time, in keys of work of one SM:
   // an SM gets the ceiling of its share of CTAs, each of which costs its keys and a
   // fixed part (kFixed), and joining costs a launch and the parts' traffic.  Few-row
-  // CTAs share an SM, whose rate one or two of them do not reach.  (Measured: 640
-  // heads x 8191 keys 162, 151, 151, 154, 170 us at 1, 2, 3, 5, 9 parts; 8 heads x
-  // 32760 keys 59, 36, 29, 31, 39 us at 4, 9, 18, 28, 64.)
+  // CTAs share an SM, whose rate one or two of them do not reach.  (Measured, one row
+  // each: 640 heads x 8191 keys 162, 146, 146, 159, 175 us at 1, 2, 3, 5, 9 parts; 8 heads x
+  // 32760 keys 55, 30, 21, 23, 30 us at 4, 9, 18, 28, 64.)
   const long long items = bh * (plan.tiles ? (R + 255) / 256 : 1);
   const double fixed = plan.tiles ? 256.0 : 350.0, join = plan.tiles ? 300.0 : 700.0;
   const int step = plan.tiles ? 64 : kRowWarps * kStep;
@@ -873,7 +878,7 @@ cudaError_t launch_kv4_rows(const ra_kv4_cache& c, const ra_kv4_attn& at, const 
   a.Hk = c.Hk; a.G = at.H / c.Hk; a.Nq = at.Nq; a.causal = at.causal; a.nsplit = plan.nsplit;
   a.scale_log2 = at.scale * kLog2e;
   const int R = a.G * a.Nq;
-  const dim3 grid(at.B * c.Hk, plan.nsplit, (R + 15) / 16);
+  const dim3 grid(at.B * c.Hk, plan.nsplit);
   if (R <= 8) return c.D == 64 ? launch_rows<64, 1>(a, grid, st) : launch_rows<128, 1>(a, grid, st);
   return c.D == 64 ? launch_rows<64, 2>(a, grid, st) : launch_rows<128, 2>(a, grid, st);
 }
