@@ -136,15 +136,15 @@ __device__ __forceinline__ Item get_item(const TileArgs& a, int item, uint32_t* 
   it.ql = a.R;
   int end;
   if constexpr (KV4) {
-    it.len = clamp_len(__ldg(a.kv_lens + it.b), a.max_pages << a.page_log2, bad);
-    it.ql = a.q_lens ? clamp_len(__ldg(a.q_lens + it.b), a.Nq, bad) : a.Nq;
+    it.len = clamp_len(ld_global(a.kv_lens + it.b), a.max_pages << a.page_log2, bad);
+    it.ql = a.q_lens ? clamp_len(ld_global(a.q_lens + it.b), a.Nq, bad) : a.Nq;
     end = it.len;
     if constexpr (MASK) {  // the furthest key that a row of the item sees
       const int last = min(it.row0 + kTiles * kRows, a.R) - 1;
       if (it.row0 / a.Nq == last / a.Nq) end = max(0, min(end, it.len - it.ql + last % a.Nq + 1));
     }
   } else {
-    it.len = a.kv_lens ? clamp_len(__ldg(a.kv_lens + it.b), a.Nk, bad) : a.Nk;
+    it.len = a.kv_lens ? clamp_len(ld_global(a.kv_lens + it.b), a.Nk, bad) : a.Nk;
     end = it.len;
   }
   const int blocks = (end + kKeys - 1) / kKeys;
@@ -374,7 +374,7 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
       auto place = [&](const Item& it, int t) -> long long {
         const int key = it.k0 + t * kKeys + row;
         if (t >= it.nb || key >= it.len) return -1;
-        int page = __ldg(a.table + static_cast<size_t>(it.b) * a.max_pages + (key >> a.page_log2));
+        int page = ld_global(a.table + static_cast<size_t>(it.b) * a.max_pages + (key >> a.page_log2));
         if (page < 0 || page >= a.num_pages) {
           bad |= kStatusBadPosition;
           page = 0;
@@ -385,8 +385,8 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
         if (at >= 0) {
           const uint4* const p = reinterpret_cast<const uint4*>(codes + at * (D / 2)) + part * kQ;
 #pragma unroll
-          for (int i = 0; i < kQ; ++i) w[i] = __ldg(p + i);
-          s = __ldg(scale + at);
+          for (int i = 0; i < kQ; ++i) w[i] = ld_global(p + i);
+          s = ld_global(scale + at);
         } else {
 #pragma unroll
           for (int i = 0; i < kQ; ++i) w[i] = make_uint4(0, 0, 0, 0);

@@ -19,9 +19,14 @@ constexpr int kNumSMs = 148;  // B200: the split of a call is planned for this m
 // promises; grid_trigger() lets the next one start.  A launch's start and a block's
 // set-up, 1 to 2 us, then lie under the end of the call before.  The trigger comes
 // after the wait, so that a kernel starts only when the one before the one before it has
-// ended: no line that that one left in an SM's first cache outlives the start.
+// ended: no line that that one left in an SM's first cache outlives the start.  Loads are
+// ordinary ones (ld_global), which see what grid_wait() makes visible: the read-only path
+// (__ldg) does not promise it for memory that is written after the kernel's start, and the
+// compiler may move it ahead of the wait.
 #ifdef __CUDACC__
 __device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+template <typename T>
+__device__ __forceinline__ T ld_global(const T* p) { return *p; }
 __device__ __forceinline__ void grid_trigger() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
 template <typename... P, typename... A>

@@ -44,7 +44,7 @@ struct CacheArgs {
 // Tokens of this CTA's sequence that the call holds; 0 for a bad count (which is reported).
 __device__ __forceinline__ int token_count(const CacheArgs& a) {
   if (!a.count) return a.T;
-  const int cnt = __ldg(a.count + blockIdx.z);
+  const int cnt = ld_global(a.count + blockIdx.z);
   if (cnt >= 0 && cnt <= a.T) return cnt;
   atomicOr(&g_kv4_status, kStatusBadPosition);
   return 0;
@@ -59,7 +59,7 @@ __device__ __forceinline__ long long token_row(const CacheArgs& a, int s, int t)
     atomicOr(&g_kv4_status, kStatusBadPosition);
     return -1;
   }
-  const int page = __ldg(a.table + static_cast<size_t>(blockIdx.z) * a.max_pages + pi);
+  const int page = ld_global(a.table + static_cast<size_t>(blockIdx.z) * a.max_pages + pi);
   if (page < 0 || page >= a.num_pages) {
     atomicOr(&g_kv4_status, kStatusBadPosition);
     return -1;
@@ -100,13 +100,13 @@ __global__ void __launch_bounds__(kThreads, kAppendPerSm) kv4_append_kernel(cons
   Raw8<kBf16> next[kAhead];
   auto load = [&](int hb, int i, Raw8<kBf16>& r) {
     const int h = hb + i / kPer, n = (i % kPer) * kNext;
-    if (h < h1 && t + n < cnt) load_raw8<kBf16>(a.x[which], src + h * a.st[which].h + n * a.st[which].n, r);
+    if (h < h1 && t + n < cnt) load_raw8<kBf16, false>(a.x[which], src + h * a.st[which].h + n * a.st[which].n, r);
     else r = Raw8<kBf16>{};
   };
 #pragma unroll
   for (int i = 0; i < kAhead; ++i) load(h0, i, next[i]);
   long long row[kPer];  // -1: not stored
-  const int s = a.start ? __ldg(a.start + blockIdx.z) : 0;
+  const int s = a.start ? ld_global(a.start + blockIdx.z) : 0;
 #pragma unroll
   for (int i = 0; i < kPer; ++i) row[i] = t + i * kNext < cnt ? token_row(a, s, t + i * kNext) : -1;
   // The maxima of kAhead rows are reduced together: each exchange halves the rows a
@@ -194,7 +194,7 @@ __global__ void __launch_bounds__(kThreads, kReadPerSm) kv4_read_kernel(const Ca
   const int h0 = (blockIdx.y - (which ? a.groups : 0)) * a.group, h1 = min(h0 + a.group, a.Hk);
   grid_wait();
   grid_trigger();
-  const int s = a.start ? __ldg(a.start + blockIdx.z) : 0;
+  const int s = a.start ? ld_global(a.start + blockIdx.z) : 0;
   const int cnt = token_count(a);
   const uint8_t* codes[kPer];
   const float* scales[kPer];  // NULL: not read
@@ -215,8 +215,8 @@ __global__ void __launch_bounds__(kThreads, kReadPerSm) kv4_read_kernel(const Ca
     scale = 0.0f;
     if (h < h1 && (kPer == 1 || scales[i % kPer])) {
       const size_t at = static_cast<size_t>(h) << a.page_log2;
-      w = __ldg(reinterpret_cast<const uint32_t*>(codes[i % kPer] + at * (kD / 2)));
-      scale = __ldg(scales[i % kPer] + at);
+      w = ld_global(reinterpret_cast<const uint32_t*>(codes[i % kPer] + at * (kD / 2)));
+      scale = ld_global(scales[i % kPer] + at);
     }
   };
 #pragma unroll
@@ -338,8 +338,8 @@ __global__ void __launch_bounds__(kRowWarps * 32, kRowsPerSm<D, NT>) kv4_rows_ke
   const int R = a.G * a.Nq;
   uint32_t bad = 0;
   grid_wait();
-  const int len = clamp_len(__ldg(a.seq_lens + b), a.max_pages << a.page_log2, &bad);
-  const int ql = a.q_lens ? clamp_len(__ldg(a.q_lens + b), a.Nq, &bad) : a.Nq;
+  const int len = clamp_len(ld_global(a.seq_lens + b), a.max_pages << a.page_log2, &bad);
+  const int ql = a.q_lens ? clamp_len(ld_global(a.q_lens + b), a.Nq, &bad) : a.Nq;
   // Steps of this CTA: [t0, t1), every kRowWarps-th for this warp.
   const int nstep = (len + kStep - 1) / kStep;
   const int per = (nstep + a.nsplit - 1) / a.nsplit;
@@ -364,7 +364,7 @@ __global__ void __launch_bounds__(kRowWarps * 32, kRowsPerSm<D, NT>) kv4_rows_ke
     const uint32_t st = ring + stage * C::kStage;
     const int left = t < t1 ? len - t * kStep : 0;  // keys of this step
     auto row_of = [&](int key0) -> uint32_t {
-      uint32_t page = static_cast<uint32_t>(__ldg(tb + (key0 >> a.page_log2)));
+      uint32_t page = static_cast<uint32_t>(ld_global(tb + (key0 >> a.page_log2)));
       if (page >= static_cast<uint32_t>(a.num_pages)) {
         bad |= kStatusBadPosition;
         page = 0;
@@ -404,7 +404,7 @@ __global__ void __launch_bounds__(kRowWarps * 32, kRowsPerSm<D, NT>) kv4_rows_ke
     const __nv_bfloat16* const src = a.q + (static_cast<size_t>(bh) * R + (in_use ? r : 0)) * D + q4 * (D / 4);
 #pragma unroll
     for (int w = 0; w < kW; ++w) {
-      qraw[j][w] = in_use ? __ldg(reinterpret_cast<const uint4*>(src + 8 * w)) : make_uint4(0, 0, 0, 0);
+      qraw[j][w] = in_use ? ld_global(reinterpret_cast<const uint4*>(src + 8 * w)) : make_uint4(0, 0, 0, 0);
       const uint32_t x[4] = {qraw[j][w].x, qraw[j][w].y, qraw[j][w].z, qraw[j][w].w};
 #pragma unroll
       for (int i = 0; i < 4; ++i)
@@ -709,7 +709,7 @@ __global__ void __launch_bounds__(128) kv4_join_kernel(Kv4Parts parts, int nspli
   grid_wait();
   grid_trigger();
   if (r >= rows) return;
-  if (q_lens && static_cast<int>(r % Nq) >= __ldg(q_lens + r / rows_b)) return;
+  if (q_lens && static_cast<int>(r % Nq) >= ld_global(q_lens + r / rows_b)) return;
   float top = -INFINITY;
   for (int s = 0; s < nsplit; ++s) top = fmaxf(top, parts.lse2[s * rows + r]);
   float sum = 0.0f, none = 0.0f, o[kC];

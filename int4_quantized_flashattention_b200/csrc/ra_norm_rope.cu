@@ -111,7 +111,7 @@ __global__ void __launch_bounds__(kThreads, 3) norm_rope_kernel(const NormArgs a
   Raw8<kBf16> next[kAhead] = {};
 #pragma unroll
   for (int i = 0; i < kAhead; ++i)
-    if (h0 + i < h1) load_raw8<kBf16>(a.x[which], src + (h0 + i) * a.st[which].h, next[i]);
+    if (h0 + i < h1) load_raw8<kBf16, false>(a.x[which], src + (h0 + i) * a.st[which].h, next[i]);
   RopePlan rp;
   HalfRows<kD> half;
   float2 cf[4];
@@ -120,14 +120,14 @@ __global__ void __launch_bounds__(kThreads, 3) norm_rope_kernel(const NormArgs a
     if constexpr (kHalf) half.init(rp, tok, c0);
     int gp[3];
 #pragma unroll
-    for (int j = 0; j < 3; ++j) gp[j] = __ldg(a.pos + 3 * nc + j);
-    rope_coef8p(a.s, rp, a.tab, gp, cf, &g_norm_status);
+    for (int j = 0; j < 3; ++j) gp[j] = ld_global(a.pos + 3 * nc + j);
+    rope_coef8p<false>(a.s, rp, a.tab, gp, cf, &g_norm_status);
   }
   float w[8], b[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    w[i] = a.weight[which] ? __ldg(a.weight[which] + c0 + i) : 1.0f;
-    b[i] = a.bias[which] ? __ldg(a.bias[which] + c0 + i) : 0.0f;
+    w[i] = a.weight[which] ? ld_global(a.weight[which] + c0 + i) : 1.0f;
+    b[i] = a.bias[which] ? ld_global(a.bias[which] + c0 + i) : 0.0f;
   }
   const size_t hn = static_cast<size_t>(a.N) * kD;
   __nv_bfloat16* dst = a.out[which] + blockIdx.z * hn * a.heads[which] + static_cast<size_t>(nc) * kD + c0;
@@ -136,7 +136,7 @@ __global__ void __launch_bounds__(kThreads, 3) norm_rope_kernel(const NormArgs a
 #pragma unroll
     for (int i = 0; i < kAhead; ++i) {
       cur[i] = next[i];
-      if (hb + kAhead + i < h1) load_raw8<kBf16>(a.x[which], src + (hb + kAhead + i) * a.st[which].h, next[i]);
+      if (hb + kAhead + i < h1) load_raw8<kBf16, false>(a.x[which], src + (hb + kAhead + i) * a.st[which].h, next[i]);
     }
 #pragma unroll
     for (int u = 0; u < kAhead; ++u) {  // heads past the last one are worked on but not stored

@@ -59,14 +59,23 @@ struct Raw8 {
   uint4 u[kBf16 ? 1 : 2];
 };
 
-template <bool kBf16>
+// A load through the read-only path, or (kConst false) an ordinary one: the read-only path is
+// for memory that nothing writes while the kernel runs, from its start on, which is not so in a
+// kernel that starts before the one ahead of it has ended.
+template <bool kConst, typename T>
+__device__ __forceinline__ T load_as(const T* p) {
+  if constexpr (kConst) return __ldg(p);
+  else return *p;
+}
+
+template <bool kBf16, bool kConst = true>
 __device__ __forceinline__ void load_raw8(const void* base, size_t elem_off, Raw8<kBf16>& r) {
   if constexpr (kBf16) {
-    r.u[0] = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(base) + elem_off));
+    r.u[0] = load_as<kConst>(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(base) + elem_off));
   } else {
     const uint4* p = reinterpret_cast<const uint4*>(static_cast<const float*>(base) + elem_off);
-    r.u[0] = __ldg(p);
-    r.u[1] = __ldg(p + 1);
+    r.u[0] = load_as<kConst>(p);
+    r.u[1] = load_as<kConst>(p + 1);
   }
 }
 
@@ -117,6 +126,7 @@ struct RopePlan {
 // Table coefficients (a, b) of the thread's 4 channel pairs for a token at grid
 // position gp (one position per segment; out-of-grid positions are reported
 // in *status and clamped so every table access stays in bounds).
+template <bool kConst = true>
 __device__ __forceinline__ void rope_coef8p(const SegInfo& s, const RopePlan& rp, const float2* tab,
                                             const int* gp, float2* cf, uint32_t* status) {
   int g[3];
@@ -132,7 +142,7 @@ __device__ __forceinline__ void rope_coef8p(const SegInfo& s, const RopePlan& rp
   for (int pr = 0; pr < 4; ++pr) {
     const int gj = rp.seg[pr] == 0 ? g[0] : (rp.seg[pr] == 1 ? g[1] : g[2]);
     const int idx = rp.off[pr] + gj * rp.stride[pr];
-    cf[pr] = __ldg(tab + idx);
+    cf[pr] = load_as<kConst>(tab + idx);
   }
 }
 
