@@ -325,7 +325,7 @@ ra_status ra_rope_rotate_quant_noalloc(const ra_problem* p, int in_dtype,
  * whose D channels are contiguous; token-major projections [B, N, H, D] are
  * {N*H*D, D, H*D}.  Every stride of an extent above 1 must be at least 1 and a
  * multiple of 16 bytes; the stride of an extent of 1 is not looked at.  Calls of
- * these operators take at most 65535 batch entries.
+ * these operators take at most 65535 batch entries (ra_attn_cross any number).
  */
 typedef struct {
   int64_t b, h, n;
@@ -350,9 +350,11 @@ ra_status ra_rope_table(const ra_problem* p, void* table, size_t bytes, void* st
 /*
  * Norm of every head's query and key row, 3D RoPE and the RoPE-aware rotation
  * (papernotes page, key design 1) in one pass:
- *   y = norm(x) * weight + bias over the D channels of each row,
+ *   y = norm(x) * weight + bias over the D channels of each row (a norm over
+ *   the channels of all heads of a token is another one, and not this),
  *   then the RoPE pairs and the rotation p->rot as ra_rope_rotate_quant applies
- *   them; fp32 throughout, rounded once to bf16.
+ *   them; fp32 throughout, rounded once to bf16.  Squares are summed in fp32:
+ *   a row of values beyond about 1e18 comes out as zeros.
  *   Hk           heads of k, >= 1 (p->H is the heads of q).
  *   norm, eps    ra_norm_mode; eps >= 0.
  *   in_dtype     element type of q and k.
@@ -377,7 +379,8 @@ ra_status ra_qk_norm_rope(const ra_problem* p, int Hk, int norm, float eps, int 
  * rint(x * fl(7/amax)) of the exact product, ties to even), for K and V alike.
  * A row whose amax is below 2^-125 gets s = 0 and codes 0; a row that holds a
  * NaN or an infinity gets s = NaN (its codes mean nothing), so that it is NaN
- * wherever it is read.  Keys go in after RoPE and, where used, the rotation (queries then carry the same rotation).
+ * wherever it is read.  Keys go in after RoPE and, where used, the rotation
+ * (queries then carry the same rotation).
  *   page_size   tokens per page: 16, 32, 64 or 128.
  *   Hk, D       heads, head dimension (64 or 128).
  *   k4, v4      [num_pages, Hk, page_size, D/2] packed codes.
@@ -423,10 +426,24 @@ ra_status ra_kv4_read(const ra_kv4_cache* c, int out_dtype, int B, int T, const 
 
 /*
  * Attention over the 4-bit cache: softmax(q k^T * scale) v with k and v the
- * cached codes times their scales, fp32 softmax and sums, P rounded to bf16
- * after its scale (codes are exact in bf16).  Forms: one or a few query rows
- * per key head split the keys over the GPU; many rows run on the tensor cores
- * in 128-row tiles.
+ * cached codes times their scales; scores, softmax and sums in fp32.  Forms: up
+ * to 16 query rows per key head split the keys over the GPU; more run on the
+ * tensor cores in 128-row tiles.  Roundings and limits:
+ *   codes       exact in what the products take; so are the queries, but for
+ *               channels 2^28 below the largest of their row in the first form.
+ *   P           times the value's scale to f16 (2^-11) in the first form; in the
+ *               tiles P, the value's scale and its product with the code.  P
+ *               times scale is held relative to the largest value scale that
+ *               the row has seen: below 2^-25 of it bits are lost (tiles under a
+ *               causal mask: below 2^-16), and values whose scale is below
+ *               2^-26 of the largest of their 32 keys lose bits in the tiles
+ *               without a mask.
+ *   scores      are off by about 2^-24 of their size; in the tiles, from 2^23 on
+ *               weights of keys within that of the largest are no longer those
+ *               of the formula.
+ * A row that holds a NaN or an infinity, or sees a key with a NaN scale, is NaN
+ * (its lse too); one that sees a value with a NaN scale is NaN.  Other rows, and
+ * rows that a mask keeps from it, are as if it were not there.
  *   B, H, Nq    sequences, query heads (a multiple of Hk: query head h reads key
  *               head h / (H / Hk)), query rows per head.
  *   max_pages   width of block_table.
@@ -468,6 +485,10 @@ ra_status ra_attn_kv4(const ra_kv4_cache* c, const ra_kv4_attn* a, const void* q
  *               reads key head h / (H / Hk)).
  *   Nq, Nk, D   query rows, key rows (>= 1), head dimension (64 or 128).
  *   scale       positive; usually 1/sqrt(D).
+ * Scores, softmax and sums are fp32, P is rounded to bf16 (2^-8).  Scores are off
+ * by about 2^-24 of their size, and from 2^28 on weights of keys within that of
+ * the largest are no longer those of the formula.  What is not finite gives NaN
+ * where the formula does.
  */
 typedef struct {
   int B, H, Hk, Nq, Nk, D;
@@ -492,8 +513,8 @@ ra_status ra_attn_cross(const ra_cross_problem* p, const void* q, const ra_strid
 /*
  * Synchronises `stream`, then reads and clears the device status word of the
  * current device.  Returns RA_OK, RA_ERR_INVALID_ARG (a kernel saw a position
- * outside the grid, or a page or length out of range), RA_ERR_TIMEOUT (an internal wait ran past its bound) or
- * RA_ERR_CUDA.
+ * outside the grid, or a page or length out of range), RA_ERR_TIMEOUT (an
+ * internal wait ran past its bound) or RA_ERR_CUDA.
  */
 ra_status ra_sync_status(void* stream);
 

@@ -7,7 +7,7 @@
 // per tile, so the tensor cores work on one block while the softmax is at the
 // other: with 128-key blocks and one buffer a tile's products and its softmax
 // took turns (890 TFLOP/s at 8192 x 8192, D = 128, softmax warps idle half of
-// the time; 1290 now).  What bounds it at D = 128: shared memory, 1280 of 1570 cycles
+// the time; 1333 now in single launches, 1200 back to back under the power cap).  What bounds it at D = 128: shared memory, 1280 of 1570 cycles
 // a block (S with N = 64 reads Q again for every block, 48 cycles an MMA against 32 of
 // arithmetic; P V 64 an MMA), and the exponentials, 1024 (8 cycles a warp
 // instruction, 16384 of them a block and partition); at D = 64 the exponentials; the
@@ -86,7 +86,8 @@ struct CfgT {
   static constexpr int kSmem = oMisc + 16 + 1024;
   // Unpacking warps: at D = 128 four for the keys and four for the values (1380 us
   // against 1453 at 1560 x 32760 x 40 heads), at D = 64, where the softmax is the
-  // slower side, four for both (1199 us against 1426).
+  // slower side, four for both (with four stages 1340 us against 1357, causal 1402
+  // against 1572).
   static constexpr bool kTwoUnpack = KV4 && D == 128;
   static constexpr int kFirstSoftmax = KV4 ? (kTwoUnpack ? 12 : 8) : 4;
   static constexpr int kThreads = (kFirstSoftmax + 8) * 32;

@@ -52,8 +52,11 @@ __device__ __forceinline__ uint32_t and_xor(uint32_t a, uint32_t b, uint32_t c) 
   return d;
 }
 
-// The codes as f16 pairs, from bits 0-3 and 16-19, and from bits 4-7 and 20-23: f16
-// has ten mantissa bits, so the second pair needs no shift (1024 + 16 (code + 8),
+// The codes as f16 pairs, from bits 0-3 and 16-19, and from bits 4-7 and 20-23.  That an
+// integer in the low mantissa bits under the exponent of 1024 is the number 1024 + integer, so
+// that one subtraction converts it, is a published method for quantised weights (Kim et al.,
+// "Who Says Elephants Can't Run", 2022); the two's complement codes enter by an exclusive-or.
+// f16 has ten mantissa bits, so the second pair needs no shift (1024 + 16 (code + 8),
 // times 1/16 and minus 72 in one exact fused operation).  Shifts and masks are what
 // bounds the kernels that unpack in registers: a word takes five of them, in bf16
 // seven.

@@ -1,6 +1,7 @@
 // Norm of every head's query and key row, 3D RoPE and the RoPE-aware rotation
-// in one pass (papernotes page, key design 1: R M q and R M k; the norms are
-// the q/k norms of the video transformers the method is applied to).
+// in one pass (papernotes page, key design 1: R M q and R M k).  The norm is over
+// the D channels of a head; a norm over all heads' channels of a token, which some
+// video transformers have instead, is not this operator.
 //
 // For each row x of D channels, in fp32:
 //   y = (x - mu) * rsqrt(mean((x - mu)^2) + eps) * w + b   (mu = 0 for RMS)

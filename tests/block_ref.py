@@ -88,10 +88,11 @@ def attention(q, k, v, ends, scale):
     error bounds of both:
       * S has D products and the key's scale in fp32: |dS| <= delta = (D + 8) u32 scale sum_d |q_d k_d| (its largest);
       * P = exp(S - m): relative error delta, plus 2^-18 for the exponential, the lazily moved reference and sums;
-      * P times the value's scale is rounded to bf16 once, the output once more.  (The few-row kernel over the cache
-        rounds to f16 instead, to 2^-11 and never worse than 2^-25 of 2^-11 times a power of two that is at most twice
-        the largest value scale: an absolute part of 2^-36 * 2 * s_max * |code| <= 2^-35 max|v| per key, divided by
-        the row's sum, which is at least 1 because a key has the reference maximum itself.)"""
+      * P is rounded to bf16 once in cross attention, the output once more.  (Both forms over the cache round to f16
+        instead, 2^-11, in the tiles the value's scale and its product with the code too: this bound is wider than
+        they need, block_bounds.py has theirs.  What is subnormal there adds an absolute part of 2^-36 * 2 * s_max *
+        |code| <= 2^-35 max|v| per key, divided by the row's sum, which is at least 1 because a key has the reference
+        maximum itself.)"""
     H, n, D = q.shape
     g = H // k.shape[0]
     out = torch.zeros(H, n, D, dtype=torch.float64, device=q.device)
