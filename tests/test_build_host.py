@@ -1,6 +1,7 @@
 """The build of the compiled binding (no GPU): libra.so does not depend on it, and one made for another torch or
 Python is made anew."""
 import os
+import shutil
 import subprocess
 import warnings
 
@@ -13,7 +14,7 @@ def b(monkeypatch, tmp_path):
     _build.build()                                      # what is there already stays
     objects = [f for f in os.listdir(_build.OBJDIR) if f.endswith(".o")]
     for f in objects:
-        os.link(os.path.join(_build.OBJDIR, f), tmp_path / f)
+        shutil.copy2(os.path.join(_build.OBJDIR, f), tmp_path / f)   # with its time
     monkeypatch.setattr(_build, "OBJDIR", str(tmp_path))
     monkeypatch.setattr(_build, "BIND", str(tmp_path / "_bind.so"))
     return _build
